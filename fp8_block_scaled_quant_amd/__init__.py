@@ -25,6 +25,16 @@ a single kernel for bf16 decode batches of up to 16 rows),
 
 ``Linear`` (in ``fp8_block_scaled_quant_amd.linear``) wraps the last one as a
 ``torch.nn.Module`` holding an E4M3 weight and its 128x128 block scales.
+
+The feed-forward operators (``libfp8bsq_ffn.so``, declared in
+``include/fp8bsq_ffn.h``):
+
+* ``gated_ffn(x, w_gate, w_gate_s, w_up, w_up_s, scale_fmt=None, out_dtype=torch.bfloat16, save=False) -> h``
+  and ``gated_ffn_backward(dh, x, g, u, w_gate, w_gate_s, w_up, w_up_s, ...) -> (dx, dw_gate, dw_up)``,
+  with ``GatedFFN``, a trainable module over both;
+* ``fp4_weight_quant(w) -> (q, s)`` and ``fp4_gemv(x, q, s, out_dtype=torch.bfloat16, bias=None) -> y``:
+  4-bit weights for the decode step;
+* ``clip_grad_norm(grads, max_norm, out=None, eps=1e-6) -> norm`` and ``grad_norm(grads) -> norm``.
 """
 
 import ctypes
@@ -34,6 +44,7 @@ import torch
 from . import _lib
 
 __all__ = ["act_quant", "weight_dequant", "weight_quant", "fp8_gemm", "act_quant_gemm", "Linear",
+           "gated_ffn", "gated_ffn_backward", "GatedFFN", "fp4_weight_quant", "fp4_gemv", "clip_grad_norm", "grad_norm",
            "Fp8Error", "library_path", "load_library"]
 
 Fp8Error = _lib.Fp8Error
@@ -234,4 +245,7 @@ def act_quant_gemm(x: torch.Tensor, b: torch.Tensor, b_s: torch.Tensor, scale_fm
     return c, y.view(torch.float8_e4m3fn), s
 
 
-from .linear import Linear  # noqa: E402  (uses the functions above)
+from .ffn import GatedFFN, gated_ffn, gated_ffn_backward  # noqa: E402  (these use the functions above)
+from .fp4 import fp4_gemv, fp4_weight_quant  # noqa: E402
+from .grad_clip import clip_grad_norm, grad_norm  # noqa: E402
+from .linear import Linear  # noqa: E402

@@ -1,4 +1,6 @@
-"""Compile the HIP sources into the in-tree shared library ``libfp8bsq.so``.
+"""Compile the HIP sources into the in-tree shared libraries ``libfp8bsq.so`` (the
+quantizers and the block-scaled GEMM) and ``libfp8bsq_ffn.so`` (the feed-forward
+operators, which call the first).
 
 gfx950 only.  Packed-FP32 instruction selection is switched off for every HIP
 source, floating-point contraction is off unless a kernel asks for a fused
@@ -18,7 +20,11 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfp8bsq.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
+FFN_LIB_NAME = "libfp8bsq_ffn.so"
+FFN_LIB_PATH = os.path.join(PKG_DIR, FFN_LIB_NAME)
+
 SOURCES = ["abi.cpp", "act_quant.hip", "weight_dequant.hip", "weight_quant.hip", "block_gemm.hip"]
+FFN_SOURCES = ["ffn_abi.cpp", "gated_ffn.hip", "gated_ffn_backward.hip", "fp4.hip", "grad_clip.hip"]
 
 HIP_FLAGS = [
     "--offload-arch=gfx950",
@@ -40,18 +46,17 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False, jobs: int = 4) -> str:
-    """Compile every source for gfx950 and link ``libfp8bsq.so``; returns its path."""
+    """Compile every source for gfx950 and link both libraries; returns ``libfp8bsq.so``'s path."""
     objdir = os.path.join(PKG_DIR, "_build")
     os.makedirs(objdir, exist_ok=True)
     cc = hipcc()
     procs = []
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(objdir, src + ".o")
-        objs.append(obj)
+    objs = {src: os.path.join(objdir, src + ".o") for src in SOURCES + FFN_SOURCES}
+    # the slowest source first, so that the others compile beside it
+    for src in sorted(objs, key=lambda s: s != "block_gemm.hip"):
         lang = ["-x", "hip"] if src.endswith(".hip") else []
         cmd = [cc, *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, *lang, "-c",
-               os.path.join(CSRC, src), "-o", obj]
+               os.path.join(CSRC, src), "-o", objs[src]]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
@@ -59,15 +64,21 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
             _drain(procs[:1])
             procs = procs[1:]
     _drain(procs)
-    tmp = LIB_PATH + ".tmp"
-    link = [cc, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
+    _link(cc, [objs[s] for s in SOURCES], [], LIB_PATH, verbose)
+    # found beside it at run time
+    _link(cc, [objs[s] for s in FFN_SOURCES], ["-L", PKG_DIR, "-lfp8bsq", "-Wl,-rpath,$ORIGIN"], FFN_LIB_PATH, verbose)
+    return LIB_PATH
+
+
+def _link(cc, objs, libs, path, verbose):
+    tmp = path + ".tmp"
+    link = [cc, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, *libs, "-o", tmp]
     if verbose:
         print(" ".join(link), file=sys.stderr)
     out = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if out.returncode != 0:
         raise RuntimeError("link failed:\n" + out.stdout.decode(errors="replace"))
-    os.replace(tmp, LIB_PATH)
-    return LIB_PATH
+    os.replace(tmp, path)
 
 
 def _drain(procs):

@@ -1,0 +1,194 @@
+// C ABI of the feed-forward operators: argument validation, workspace layout
+// and dispatch.  Every check runs before any HIP call, so a rejected call
+// queues nothing.
+#include <stddef.h>
+#include <stdint.h>
+
+#include "ffn_launch.h"
+#include "fp8bsq_ffn.h"
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 31;         // per-dimension limit of the launch grids
+constexpr int64_t kMaxRows = (int64_t)65535 * 16;     // grid.y limit of the smallest row tile
+constexpr int64_t kMaxFeatures = (int64_t)65535 * 32; // grid.y limit over 2 f features in tiles of 64
+
+bool aligned(const void *p, uintptr_t bytes) { return ((uintptr_t)p % bytes) == 0; }
+bool known_dtype(int d) { return d == FP8BSQ_F32 || d == FP8BSQ_BF16; }
+uintptr_t size_of(int dtype) { return dtype == FP8BSQ_F32 ? 4 : 2; }
+int launch_status(hipError_t e) { return e == hipSuccess ? FP8BSQ_OK : FP8BSQ_ELAUNCH; }
+
+// Pieces of a workspace, each 256-byte aligned.
+struct Layout {
+  size_t bytes = 0;
+  size_t add(int64_t n) {
+    const size_t at = bytes;
+    bytes += ((size_t)n + 255) / 256 * 256;
+    return at;
+  }
+};
+
+bool ffn_sizes_ok(int64_t m, int64_t f, int64_t k) {
+  return m > 0 && f > 0 && k > 0 && k % 128 == 0 && m <= kMaxRows && f < kMaxDim && k < kMaxDim;
+}
+
+// Workspace of the forward pass: x's codes and scales.
+struct ForwardSpace : Layout {
+  size_t a, a_s;
+  ForwardSpace(int64_t m, int64_t k) {
+    a = add(m * k);
+    a_s = add(m * (k / 128) * 4);
+  }
+};
+
+// Workspace of the backward pass.
+struct BackwardSpace : Layout {
+  size_t rq, rs, wt, wt_s, split, split_bytes, cq, ce, xq, xe;
+  BackwardSpace(int64_t m, int64_t f, int64_t k) {
+    rq = add(m * 2 * f);
+    rs = add(m * (2 * f / 128) * 4);
+    wt = add(k * 2 * f);
+    wt_s = add((k / 128) * (2 * f / 128) * 4);
+    split_bytes = fp8_block_gemm_split_workspace(m, k, 2 * f);
+    split = add((int64_t)split_bytes);
+    cq = add(2 * f * fp8bsq::tokens_padded(m));
+    ce = add(fp8bsq::token_exp_bytes(2 * f, m));
+    xq = add(k * fp8bsq::tokens_padded(m));
+    xe = add(fp8bsq::token_exp_bytes(k, m));
+  }
+};
+
+}  // namespace
+
+extern "C" {
+
+size_t fp8_gated_ffn_workspace(int64_t m, int64_t f, int64_t k) {
+  return ffn_sizes_ok(m, f, k) ? ForwardSpace(m, k).bytes : 0;
+}
+
+int fp8_gated_ffn(const void *x, int x_dtype, int scale_fmt, const uint8_t *w_gate, const float *w_gate_s,
+                  const uint8_t *w_up, const float *w_up_s, void *h, void *g, void *u, int out_dtype, int64_t m,
+                  int64_t f, int64_t k, void *workspace, size_t workspace_bytes, void *hip_stream) {
+  if (m < 0 || f < 0 || k <= 0) return FP8BSQ_EINVAL;
+  if (!known_dtype(x_dtype) || !known_dtype(out_dtype)) return FP8BSQ_EINVAL;
+  if (scale_fmt != FP8BSQ_SCALE_NONE && scale_fmt != FP8BSQ_SCALE_UE8M0) return FP8BSQ_EINVAL;
+  if (k % 128 != 0) return FP8BSQ_ESHAPE;
+  if (m == 0 || f == 0) return FP8BSQ_OK;
+  if (!x || !w_gate || !w_gate_s || !w_up || !w_up_s || !h || !workspace || !g != !u) return FP8BSQ_EINVAL;
+  const uintptr_t out = size_of(out_dtype);
+  if (!aligned(x, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(w_gate_s, 4) ||
+      !aligned(w_up_s, 4) || !aligned(h, out) || !aligned(g, out) || !aligned(u, out) || !aligned(workspace, 256))
+    return FP8BSQ_EALIGN;
+  if (!ffn_sizes_ok(m, f, k)) return FP8BSQ_ERANGE;
+  const ForwardSpace ws(m, k);
+  if (workspace_bytes < ws.bytes) return FP8BSQ_ESCRATCH;
+  uint8_t *a = (uint8_t *)workspace + ws.a;
+  float *a_s = (float *)((uint8_t *)workspace + ws.a_s);
+  const int rc = fp8_act_quant(x, x_dtype, m, k, 128, scale_fmt, a, a_s, hip_stream);
+  if (rc != FP8BSQ_OK) return rc;
+  return launch_status(fp8bsq::launch_gated_gemm(a, a_s, w_gate, w_gate_s, w_up, w_up_s, h, g, u,
+                                                 out_dtype == FP8BSQ_BF16, m, f, k, (hipStream_t)hip_stream));
+}
+
+size_t fp8_gated_ffn_backward_workspace(int64_t m, int64_t f, int64_t k) {
+  return ffn_sizes_ok(m, f, k) && f % 128 == 0 && f <= kMaxFeatures ? BackwardSpace(m, f, k).bytes : 0;
+}
+
+int fp8_gated_ffn_backward(const void *dh, const void *x, const void *g, const void *u, int in_dtype,
+                           const uint8_t *w_gate, const float *w_gate_s, const uint8_t *w_up,
+                           const float *w_up_s, void *dx, void *dw_gate, void *dw_up, int out_dtype, int64_t m,
+                           int64_t f, int64_t k, void *workspace, size_t workspace_bytes, void *hip_stream) {
+  if (m < 0 || f <= 0 || k <= 0) return FP8BSQ_EINVAL;
+  if (!known_dtype(in_dtype) || !known_dtype(out_dtype)) return FP8BSQ_EINVAL;
+  if (f % 128 != 0 || k % 128 != 0) return FP8BSQ_ESHAPE;
+  if (!dw_gate != !dw_up) return FP8BSQ_EINVAL;
+  const hipStream_t st = (hipStream_t)hip_stream;
+  const bool in_bf16 = in_dtype == FP8BSQ_BF16, out_bf16 = out_dtype == FP8BSQ_BF16;
+  if (m == 0) {
+    if (!dw_gate) return FP8BSQ_OK;
+    if (!aligned(dw_gate, 4) || !aligned(dw_up, 4)) return FP8BSQ_EALIGN;
+    if (f > kMaxFeatures || k >= kMaxDim) return FP8BSQ_ERANGE;
+    // no tokens: the product over an empty contraction
+    return launch_status(fp8bsq::launch_weight_grad(nullptr, nullptr, nullptr, nullptr, dw_gate, dw_up, out_bf16, 0,
+                                                    f, k, st));
+  }
+  if (!dx && !dw_gate) return FP8BSQ_OK;
+  if (!dh || !g || !u || !workspace || (dx && (!w_gate || !w_gate_s || !w_up || !w_up_s)) || (dw_gate && !x))
+    return FP8BSQ_EINVAL;
+  if (!aligned(dh, 16) || !aligned(g, 16) || !aligned(u, 16) || !aligned(x, 16) || !aligned(w_gate, 16) ||
+      !aligned(w_up, 16) || !aligned(w_gate_s, 4) || !aligned(w_up_s, 4) || !aligned(dx, 4) ||
+      !aligned(dw_gate, 4) || !aligned(dw_up, 4) || !aligned(workspace, 256))
+    return FP8BSQ_EALIGN;
+  if (!ffn_sizes_ok(m, f, k) || f > kMaxFeatures) return FP8BSQ_ERANGE;
+  const BackwardSpace ws(m, f, k);
+  if (workspace_bytes < ws.bytes) return FP8BSQ_ESCRATCH;
+  uint8_t *base = (uint8_t *)workspace;
+  uint8_t *rq = base + ws.rq, *cq = base + ws.cq, *ce = base + ws.ce;
+  float *rs = (float *)(base + ws.rs);
+  int rc = launch_status(fp8bsq::launch_ffn_grad_quant(dh, g, u, in_bf16, m, f, dx ? rq : nullptr, rs,
+                                                       dw_gate ? cq : nullptr, ce, st));
+  if (rc != FP8BSQ_OK) return rc;
+  if (dx) {
+    uint8_t *wt = base + ws.wt;
+    float *wt_s = (float *)(base + ws.wt_s);
+    rc = launch_status(fp8bsq::launch_weights_transpose(w_gate, w_gate_s, w_up, w_up_s, f, k, wt, wt_s, st));
+    if (rc != FP8BSQ_OK) return rc;
+    rc = fp8_block_gemm_split(rq, rs, wt, wt_s, dx, out_dtype, m, k, 2 * f, FP8BSQ_SCALE_UE8M0,
+                              ws.split_bytes ? base + ws.split : nullptr, ws.split_bytes, hip_stream);
+    if (rc != FP8BSQ_OK) return rc;
+  }
+  if (!dw_gate) return FP8BSQ_OK;
+  uint8_t *xq = base + ws.xq, *xe = base + ws.xe;
+  rc = launch_status(fp8bsq::launch_token_quant(x, in_bf16, m, k, xq, xe, st));
+  if (rc != FP8BSQ_OK) return rc;
+  return launch_status(fp8bsq::launch_weight_grad(cq, ce, xq, xe, dw_gate, dw_up, out_bf16, m, f, k, st));
+}
+
+int fp4_weight_quant(const void *w, int w_dtype, int64_t n, int64_t k, uint8_t *q, uint8_t *s, void *hip_stream) {
+  if (n < 0 || k < 0) return FP8BSQ_EINVAL;
+  if (!known_dtype(w_dtype)) return FP8BSQ_EINVAL;
+  if (k % 32 != 0) return FP8BSQ_ESHAPE;
+  if (n == 0 || k == 0) return FP8BSQ_OK;
+  if (!w || !q || !s) return FP8BSQ_EINVAL;
+  if (!aligned(w, 16) || !aligned(q, 4)) return FP8BSQ_EALIGN;
+  if (n >= kMaxDim || k >= kMaxDim || n * (k / 32) >= (int64_t)1 << 37) return FP8BSQ_ERANGE;
+  return launch_status(
+      fp8bsq::launch_fp4_weight_quant(w, w_dtype == FP8BSQ_BF16, n, k, q, s, (hipStream_t)hip_stream));
+}
+
+int fp4_gemv(const void *x, int x_dtype, const uint8_t *q, const uint8_t *s, const void *bias, void *y,
+             int y_dtype, int64_t m, int64_t n, int64_t k, void *hip_stream) {
+  if (m < 0 || n < 0 || k <= 0) return FP8BSQ_EINVAL;
+  if (!known_dtype(x_dtype) || !known_dtype(y_dtype)) return FP8BSQ_EINVAL;
+  if (k % 32 != 0) return FP8BSQ_ESHAPE;
+  if (m == 0 || n == 0) return FP8BSQ_OK;
+  if (!x || !q || !s || !y) return FP8BSQ_EINVAL;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(bias, size_of(y_dtype)) || !aligned(y, size_of(y_dtype)))
+    return FP8BSQ_EALIGN;
+  if (m > kMaxRows || n >= kMaxDim || k >= kMaxDim) return FP8BSQ_ERANGE;
+  return launch_status(fp8bsq::launch_fp4_gemv(x, x_dtype == FP8BSQ_BF16, q, s, bias, y, y_dtype == FP8BSQ_BF16, m,
+                                               n, k, (hipStream_t)hip_stream));
+}
+
+size_t fp8bsq_clip_grad_norm_workspace(int64_t count) { return count < 0 ? 0 : fp8bsq::clip_workspace_bytes(count); }
+
+int fp8bsq_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *numels,
+                          const int32_t *dtypes, int64_t count, float max_norm, float eps, float *norm,
+                          void *workspace, size_t workspace_bytes, void *hip_stream) {
+  if (count < 0 || !(max_norm >= 0.0f) || !(eps >= 0.0f)) return FP8BSQ_EINVAL;
+  if (!norm || !workspace || (count > 0 && (!grads || !numels || !dtypes))) return FP8BSQ_EINVAL;
+  for (int64_t i = 0; i < count; ++i) {
+    if (numels[i] < 0 || !known_dtype(dtypes[i])) return FP8BSQ_EINVAL;
+    if (numels[i] > 0 && (!grads[i] || (outs && !outs[i]))) return FP8BSQ_EINVAL;
+    const uintptr_t size = size_of(dtypes[i]);
+    if (!aligned(grads[i], size) || (outs && !aligned(outs[i], size))) return FP8BSQ_EALIGN;
+    if (numels[i] >= (int64_t)1 << 48) return FP8BSQ_ERANGE;
+  }
+  if (!aligned(norm, 4) || !aligned(workspace, 256)) return FP8BSQ_EALIGN;
+  if (count > kMaxDim / 1024) return FP8BSQ_ERANGE;
+  if (workspace_bytes < fp8bsq::clip_workspace_bytes(count)) return FP8BSQ_ESCRATCH;
+  return launch_status(fp8bsq::launch_clip_grad_norm(grads, outs, numels, dtypes, count, max_norm, eps, norm,
+                                                     workspace, (hipStream_t)hip_stream));
+}
+
+}  // extern "C"

@@ -16,6 +16,8 @@ It is a plain, slow, obviously-correct statement of what the method computes:
 * ``fp8_gemm``        -- the block-scaled FP8 GEMM, each 128-wide K slice's
                          partial sum scaled and accumulated, in float64, plus the
                          per-element error bound GPU results are held to.
+* ``ffn``             -- the gated feed-forward block and its backward pass.
+* ``fp4``             -- 4-bit weights with a power-of-two scale per 32.
 
 Every reading taken where the pages leave a step open is stated in the
 docstring of the function that takes it.  Parity status: every function here is
@@ -24,7 +26,7 @@ numbers (the <0.25% training-loss figure and the FP32 promotion interval on
 H800 hardware): those are "parity unpinned" and nothing here computes them.
 """
 
-from . import e4m3  # noqa: F401
+from . import e4m3, ffn, fp4  # noqa: F401
 from .act_quant import act_quant  # noqa: F401
 from .weight_dequant import weight_dequant, f32_to_bf16_bits, bf16_bits_to_f32  # noqa: F401
 from .weight_quant import weight_quant  # noqa: F401
