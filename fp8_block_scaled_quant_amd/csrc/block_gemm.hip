@@ -19,6 +19,7 @@
 #include <atomic>
 
 #include "fp8bsq.h"
+#include "device_cus.h"
 #include "launch.h"
 #include "mfma_tile.h"
 #include "quant_common.h"
@@ -1183,24 +1184,6 @@ __global__ __launch_bounds__(64 * (kAT + 2)) void block_gemm_decode_wide_kernel(
 }
 
 }  // namespace
-
-// Compute units of the current device, asked of the runtime once per device;
-// 0 if the runtime cannot say.
-static int current_device_cus() {
-  constexpr int kMaxDevices = 64;
-  static std::atomic<int> cached[kMaxDevices];   // 0: not asked yet
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 0;
-  if (dev < kMaxDevices) {
-    const int c = cached[dev].load(std::memory_order_relaxed);
-    if (c > 0) return c;
-  }
-  int cus = 0;
-  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-    return 0;
-  if (dev < kMaxDevices) cached[dev].store(cus, std::memory_order_relaxed);
-  return cus;
-}
 
 // Compute waves of the decode kernel and the fused path, or weight tiles of
 // the wide decode kernel, per workgroup for a weight of n rows: the fewest

@@ -87,7 +87,7 @@ int fp8_gated_ffn(const void *x, int x_dtype, int scale_fmt, const uint8_t *w_ga
   const int rc = fp8_act_quant(x, x_dtype, m, k, 128, scale_fmt, a, a_s, hip_stream);
   if (rc != FP8BSQ_OK) return rc;
   return launch_status(fp8bsq::launch_gated_gemm(a, a_s, w_gate, w_gate_s, w_up, w_up_s, h, g, u,
-                                                 out_dtype == FP8BSQ_BF16, m, f, k, (hipStream_t)hip_stream));
+                                                 scale_fmt == FP8BSQ_SCALE_UE8M0, out_dtype == FP8BSQ_BF16, m, f, k, (hipStream_t)hip_stream));
 }
 
 size_t fp8_gated_ffn_backward_workspace(int64_t m, int64_t f, int64_t k) {

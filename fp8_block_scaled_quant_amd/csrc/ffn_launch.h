@@ -10,11 +10,12 @@
 namespace fp8bsq {
 
 // h = silu(g) * u with g, u [m, f] the block-scaled products of the codes a
-// [m, k] (scales a_s) and the weights wg, wu [f, k].  g_out, u_out: both null,
-// or both receive g and u.
+// [m, k] (scales a_s; a_s_pow2: all powers of two) and the weights wg, wu
+// [f, k].  g_out, u_out: both null, or both receive g and u.
 hipError_t launch_gated_gemm(const uint8_t *a, const float *a_s, const uint8_t *wg, const float *wg_s,
                              const uint8_t *wu, const float *wu_s, void *h, void *g_out, void *u_out,
-                             bool out_bf16, int64_t m, int64_t f, int64_t k, hipStream_t stream);
+                             bool a_s_pow2, bool out_bf16, int64_t m, int64_t f, int64_t k,
+                             hipStream_t stream);
 
 // Columns of the quantized-along-tokens operands: m rounded up to whole blocks.
 inline int64_t tokens_padded(int64_t m) { return (m + 127) / 128 * 128; }
