@@ -106,7 +106,7 @@ int fp8_gated_ffn_backward(const void *dh, const void *x, const void *g, const v
   const bool in_bf16 = in_dtype == FP8BSQ_BF16, out_bf16 = out_dtype == FP8BSQ_BF16;
   if (m == 0) {
     if (!dw_gate) return FP8BSQ_OK;
-    if (!aligned(dw_gate, 4) || !aligned(dw_up, 4)) return FP8BSQ_EALIGN;
+    if (!aligned(dw_gate, 16) || !aligned(dw_up, 16)) return FP8BSQ_EALIGN;
     if (f > kMaxFeatures || k >= kMaxDim) return FP8BSQ_ERANGE;
     // no tokens: the product over an empty contraction
     return launch_status(fp8bsq::launch_weight_grad(nullptr, nullptr, nullptr, nullptr, dw_gate, dw_up, out_bf16, 0,
@@ -117,7 +117,7 @@ int fp8_gated_ffn_backward(const void *dh, const void *x, const void *g, const v
     return FP8BSQ_EINVAL;
   if (!aligned(dh, 16) || !aligned(g, 16) || !aligned(u, 16) || !aligned(x, 16) || !aligned(w_gate, 16) ||
       !aligned(w_up, 16) || !aligned(w_gate_s, 4) || !aligned(w_up_s, 4) || !aligned(dx, 4) ||
-      !aligned(dw_gate, 4) || !aligned(dw_up, 4) || !aligned(workspace, 256))
+      !aligned(dw_gate, 16) || !aligned(dw_up, 16) || !aligned(workspace, 256))
     return FP8BSQ_EALIGN;
   if (!ffn_sizes_ok(m, f, k) || f > kMaxFeatures) return FP8BSQ_ERANGE;
   const BackwardSpace ws(m, f, k);

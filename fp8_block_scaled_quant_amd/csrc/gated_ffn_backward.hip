@@ -13,6 +13,7 @@
 // dx is the block-scaled GEMM of [dg | du] (m x 2 f) and [Wg^T | Wu^T]
 // (k x 2 f).  dW is a product with power-of-two scales on both operands: both
 // go into the MFMA, which then accumulates over the whole contraction.
+#include "device_cus.h"
 #include "ffn_launch.h"
 #include "mfma_tile.h"
 #include "pow2_scale.h"
@@ -228,53 +229,139 @@ __global__ __launch_bounds__(256) void weights_transpose_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// dW: 256 threads = 2 x 2 waves, each wave a 32 x 32 output tile, fragments
-// straight from global memory; f and k are multiples of 128, so no edges.
+// dW [2 f, k] = dgu^T x over the tokens.  Power-of-two scales on both operands
+// go into the MFMA (one exponent per row and 128 tokens, which is the MFMA's
+// whole K), so the matrix core accumulates by itself and no vector instruction
+// touches an accumulator before the epilogue.
+//
+// Workgroup tile 256 x 256, 512 threads = 8 waves, 2 (dgu rows) x 4 (x rows),
+// each 128 x 64: acc[8][4] tiles of 16 x 16.  Operands come by direct
+// global->LDS transfers into a two-stage ring (token block mb + 1 while mb is
+// computed); exponents come from memory straight to registers, one word of four
+// token blocks per fragment row, a chunk ahead.  The x rows are the MFMA's row
+// operand, so a lane holds four consecutive columns of a dW row.
 // ---------------------------------------------------------------------------
+constexpr int kDwTile = 256, kDwThreads = 512;
+
+struct DwSmem {
+  uint8_t a[2][kDwTile * kBlock];   // dgu rows
+  uint8_t b[2][kDwTile * kBlock];   // x rows
+};
+
+// Tile of workgroup turn `it`: each XCD (workgroups are dealt to the eight
+// round-robin) walks a contiguous share of the tiles, in groups of four dgu
+// tiles across x's.
+__device__ __forceinline__ void dw_tile_coords(int it, int tiles_r, int tiles_c, int &tr, int &tc) {
+  const int ntiles = tiles_r * tiles_c, base = ntiles / 8, rest = ntiles % 8, xcd = it % 8;
+  const int tile = xcd * base + min(xcd, rest) + it / 8;
+  constexpr int kGroup = 4;
+  const int group = tile / (kGroup * tiles_c), first = group * kGroup;
+  const int gr = min(tiles_r - first, kGroup), idx = tile - group * kGroup * tiles_c;
+  tr = first + idx % gr;
+  tc = idx / gr;
+}
+
 template <bool kBf16Out>
-__global__ __launch_bounds__(256) void weight_grad_simple_kernel(
+__global__ __launch_bounds__(kDwThreads) void weight_grad_tile_kernel(
     const uint8_t *__restrict__ dq, const uint32_t *__restrict__ de, const uint8_t *__restrict__ xq,
     const uint32_t *__restrict__ xe, void *__restrict__ dwg, void *__restrict__ dwu, int64_t mpad, int64_t f,
-    int64_t k) {
-  const int nmb = (int)(mpad / kBlock);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t r0 = (int64_t)blockIdx.y * 64 + (wave >> 1) * 32, c0 = (int64_t)blockIdx.x * 64 + (wave & 1) * 32;
-  const int lr = lane & 15, lk = (lane >> 4) * 32, lq = (lane >> 4) * 4;
-  f32x4 acc[2][2];
+    int64_t k, int tiles_r, int tiles_c) {
+  __shared__ __attribute__((aligned(1024))) DwSmem sm;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nmb = (int)(mpad / kBlock), ntiles = tiles_r * tiles_c;
+  const int64_t rows = 2 * f;
+  const int wr = (wave >> 2) * 128, wc = (wave & 3) * 64;
+  const int fr = lane & 15, fq = lane >> 4, dr = lane >> 3, ds = lane & 7;
+  const uint32_t lds_a = lds_addr(&sm.a[0][0]), lds_b = lds_addr(&sm.b[0][0]);
+  for (int it = blockIdx.x; it < ntiles; it += gridDim.x) {
+    int tr, tc;
+    dw_tile_coords(it, tiles_r, tiles_c, tr, tc);
+    const int64_t r0 = (int64_t)tr * kDwTile, c0 = (int64_t)tc * kDwTile;
+    // 8-row groups 4 wave .. + 3 of both operands; rows past the matrix re-read its last
+    uint32_t a_off[4], b_off[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int mb = 0; mb < nmb; ++mb) {
-    i32x8 af[2], bf[2];
-    int ea[2], eb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t ra = r0 + 16 * i + lr, rb = c0 + 16 * i + lr;
-      af[i] = load_frag(dq + ra * mpad + (int64_t)mb * kBlock + lk);
-      bf[i] = load_frag(xq + rb * mpad + (int64_t)mb * kBlock + lk);
-      ea[i] = (int)((de[(mb >> 2) * (2 * f) + ra] >> (8 * (mb & 3))) & 0xFFu);
-      eb[i] = (int)((xe[(mb >> 2) * k + rb] >> (8 * (mb & 3))) & 0xFFu);
+    for (int i = 0; i < 4; ++i) {
+      const int row = 8 * (4 * wave + i) + dr;
+      const int chunk = (ds ^ swz(row)) << 4;
+      a_off[i] = (uint32_t)((min(r0 + row, rows - 1) - r0) * mpad + chunk);
+      b_off[i] = (uint32_t)((min(c0 + row, k - 1) - c0) * mpad + chunk);
     }
+    const uint8_t *a_base = dq + r0 * mpad, *b_base = xq + c0 * mpad;
+    auto issue = [&](int mb, int s) {
+      const int64_t at = (int64_t)mb * kBlock;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j], acc[i][j], 0, 0, 0, ea[i], 0,
-                                                                     eb[j]);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t row = r0 + 16 * i + lq + e, col = c0 + 16 * j + lr;
-        if (row < f)
-          store_out(dwg, kBf16Out, row * k + col, acc[i][j][e]);
-        else
-          store_out(dwu, kBf16Out, (row - f) * k + col, acc[i][j][e]);
+      for (int i = 0; i < 4; ++i) {
+        lds_dma16(a_base + at, a_off[i], lds_a + s * (kDwTile * kBlock) + (4 * wave + i) * 1024);
+        lds_dma16(b_base + at, b_off[i], lds_b + s * (kDwTile * kBlock) + (4 * wave + i) * 1024);
       }
+    };
+    uint32_t ea[8], eb[4], ea_next[8], eb_next[4];
+    auto load_exps = [&](int chunk) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ea_next[i] = de[(int64_t)chunk * rows + min(r0 + wr + 16 * i + fr, rows - 1)];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) eb_next[j] = xe[(int64_t)chunk * k + min(c0 + wc + 16 * j + fr, k - 1)];
+    };
+    f32x4 acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (nmb > 0) {
+      issue(0, 0);
+      load_exps(0);
+    }
+#pragma nounroll
+    for (int mb = 0; mb < nmb; ++mb) {
+      const int cur = mb & 1;
+      wait_dma_all();
+      workgroup_barrier();   // stage cur landed for every wave; stage cur ^ 1 no longer read
+      if ((mb & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ea[i] = ea_next[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) eb[j] = eb_next[j];
+        if (mb + 4 < nmb) load_exps(mb / 4 + 1);
+      }
+      if (mb + 1 < nmb) issue(mb + 1, cur ^ 1);
+      i32x8 bf[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = wc + 16 * j + fr;
+        bf[j] = frag_from_lds(&sm.b[cur][r * kBlock], fq, r);
+      }
+      const int shift = 8 * (mb & 3);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = wr + 16 * i + fr;
+        const i32x8 af = frag_from_lds(&sm.a[cur][r * kBlock], fq, r);
+        const int sa = (int)((ea[i] >> shift) & 0xFFu);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af, acc[i][j], 0, 0, 0,
+                                                                       (int)((eb[j] >> shift) & 0xFFu), 0, sa);
+      }
+    }
+    workgroup_barrier();   // every wave is done with LDS before the next tile's transfers
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = r0 + wr + 16 * i + fr;
+      if (row >= rows) continue;
+      void *out = row < f ? dwg : dwu;
+      const int64_t at = (row < f ? row : row - f) * k;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t col = c0 + wc + 16 * j + 4 * fq;
+        if (col >= k) continue;   // k is a multiple of 128: four columns are in or out together
+        const f32x4 v = acc[i][j];
+        if (kBf16Out)
+          *(u32x2 *)((uint16_t *)out + at + col) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        else
+          *(f32x4 *)((float *)out + at + col) = v;
+      }
+    }
+  }
 }
 
 }  // namespace
@@ -314,13 +401,16 @@ hipError_t launch_weight_grad(const uint8_t *dq, const uint8_t *de, const uint8_
                               void *dwg, void *dwu, bool out_bf16, int64_t m, int64_t f, int64_t k,
                               hipStream_t stream) {
   const int64_t mpad = tokens_padded(m);
-  const dim3 grid((unsigned)(k / 64), (unsigned)(2 * f / 64)), block(256);
+  const int64_t tiles_r = (2 * f + kDwTile - 1) / kDwTile, tiles_c = (k + kDwTile - 1) / kDwTile;
+  int cus = current_device_cus();
+  if (cus <= 0) cus = 256;
+  const dim3 grid((unsigned)(tiles_r * tiles_c < cus ? tiles_r * tiles_c : cus)), block(kDwThreads);
   if (out_bf16)
-    hipLaunchKernelGGL(weight_grad_simple_kernel<true>, grid, block, 0, stream, dq, (const uint32_t *)de, xq,
-                       (const uint32_t *)xe, dwg, dwu, mpad, f, k);
+    hipLaunchKernelGGL(weight_grad_tile_kernel<true>, grid, block, 0, stream, dq, (const uint32_t *)de, xq,
+                       (const uint32_t *)xe, dwg, dwu, mpad, f, k, (int)tiles_r, (int)tiles_c);
   else
-    hipLaunchKernelGGL(weight_grad_simple_kernel<false>, grid, block, 0, stream, dq, (const uint32_t *)de, xq,
-                       (const uint32_t *)xe, dwg, dwu, mpad, f, k);
+    hipLaunchKernelGGL(weight_grad_tile_kernel<false>, grid, block, 0, stream, dq, (const uint32_t *)de, xq,
+                       (const uint32_t *)xe, dwg, dwu, mpad, f, k, (int)tiles_r, (int)tiles_c);
   return hipGetLastError();
 }
 
