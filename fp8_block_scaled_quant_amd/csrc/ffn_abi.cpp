@@ -11,59 +11,24 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;         // per-dimension limit of the launch grids
 constexpr int64_t kMaxRows = (int64_t)65535 * 16;     // grid.y limit of the smallest row tile
-constexpr int64_t kMaxFeatures = (int64_t)65535 * 32; // grid.y limit over 2 f features in tiles of 64
+constexpr int64_t kMaxFeatures = (int64_t)1 << 21;    // features and K of the feed-forward block
 
 bool aligned(const void *p, uintptr_t bytes) { return ((uintptr_t)p % bytes) == 0; }
 bool known_dtype(int d) { return d == FP8BSQ_F32 || d == FP8BSQ_BF16; }
 uintptr_t size_of(int dtype) { return dtype == FP8BSQ_F32 ? 4 : 2; }
 int launch_status(hipError_t e) { return e == hipSuccess ? FP8BSQ_OK : FP8BSQ_ELAUNCH; }
 
-// Pieces of a workspace, each 256-byte aligned.
-struct Layout {
-  size_t bytes = 0;
-  size_t add(int64_t n) {
-    const size_t at = bytes;
-    bytes += ((size_t)n + 255) / 256 * 256;
-    return at;
-  }
-};
-
+// Rows reach the tile kernels by 32-bit offsets from their tile.
 bool ffn_sizes_ok(int64_t m, int64_t f, int64_t k) {
-  return m > 0 && f > 0 && k > 0 && k % 128 == 0 && m <= kMaxRows && f < kMaxDim && k < kMaxDim;
+  return m > 0 && f > 0 && k > 0 && k % 128 == 0 && m <= kMaxRows && f <= kMaxFeatures && k <= kMaxFeatures;
 }
-
-// Workspace of the forward pass: x's codes and scales.
-struct ForwardSpace : Layout {
-  size_t a, a_s;
-  ForwardSpace(int64_t m, int64_t k) {
-    a = add(m * k);
-    a_s = add(m * (k / 128) * 4);
-  }
-};
-
-// Workspace of the backward pass.
-struct BackwardSpace : Layout {
-  size_t rq, rs, wt, wt_s, split, split_bytes, cq, ce, xq, xe;
-  BackwardSpace(int64_t m, int64_t f, int64_t k) {
-    rq = add(m * 2 * f);
-    rs = add(m * (2 * f / 128) * 4);
-    wt = add(k * 2 * f);
-    wt_s = add((k / 128) * (2 * f / 128) * 4);
-    split_bytes = fp8_block_gemm_split_workspace(m, k, 2 * f);
-    split = add((int64_t)split_bytes);
-    cq = add(2 * f * fp8bsq::tokens_padded(m));
-    ce = add(fp8bsq::token_exp_bytes(2 * f, m));
-    xq = add(k * fp8bsq::tokens_padded(m));
-    xe = add(fp8bsq::token_exp_bytes(k, m));
-  }
-};
 
 }  // namespace
 
 extern "C" {
 
 size_t fp8_gated_ffn_workspace(int64_t m, int64_t f, int64_t k) {
-  return ffn_sizes_ok(m, f, k) ? ForwardSpace(m, k).bytes : 0;
+  return ffn_sizes_ok(m, f, k) ? fp8bsq::gated_space(m, f, k).bytes : 0;
 }
 
 int fp8_gated_ffn(const void *x, int x_dtype, int scale_fmt, const uint8_t *w_gate, const float *w_gate_s,
@@ -80,18 +45,14 @@ int fp8_gated_ffn(const void *x, int x_dtype, int scale_fmt, const uint8_t *w_ga
       !aligned(w_up_s, 4) || !aligned(h, out) || !aligned(g, out) || !aligned(u, out) || !aligned(workspace, 256))
     return FP8BSQ_EALIGN;
   if (!ffn_sizes_ok(m, f, k)) return FP8BSQ_ERANGE;
-  const ForwardSpace ws(m, k);
-  if (workspace_bytes < ws.bytes) return FP8BSQ_ESCRATCH;
-  uint8_t *a = (uint8_t *)workspace + ws.a;
-  float *a_s = (float *)((uint8_t *)workspace + ws.a_s);
-  const int rc = fp8_act_quant(x, x_dtype, m, k, 128, scale_fmt, a, a_s, hip_stream);
-  if (rc != FP8BSQ_OK) return rc;
-  return launch_status(fp8bsq::launch_gated_gemm(a, a_s, w_gate, w_gate_s, w_up, w_up_s, h, g, u,
-                                                 scale_fmt == FP8BSQ_SCALE_UE8M0, out_dtype == FP8BSQ_BF16, m, f, k, (hipStream_t)hip_stream));
+  if (workspace_bytes < fp8bsq::gated_space(m, f, k).bytes) return FP8BSQ_ESCRATCH;
+  return launch_status(fp8bsq::launch_gated_ffn(x, x_dtype == FP8BSQ_BF16, scale_fmt == FP8BSQ_SCALE_UE8M0, w_gate,
+                                                w_gate_s, w_up, w_up_s, h, g, u, out_dtype == FP8BSQ_BF16, m, f, k,
+                                                workspace, (hipStream_t)hip_stream));
 }
 
 size_t fp8_gated_ffn_backward_workspace(int64_t m, int64_t f, int64_t k) {
-  return ffn_sizes_ok(m, f, k) && f % 128 == 0 && f <= kMaxFeatures ? BackwardSpace(m, f, k).bytes : 0;
+  return ffn_sizes_ok(m, f, k) && f % 128 == 0 ? fp8bsq::backward_space(m, f, k).bytes : 0;
 }
 
 int fp8_gated_ffn_backward(const void *dh, const void *x, const void *g, const void *u, int in_dtype,
@@ -107,10 +68,11 @@ int fp8_gated_ffn_backward(const void *dh, const void *x, const void *g, const v
   if (m == 0) {
     if (!dw_gate) return FP8BSQ_OK;
     if (!aligned(dw_gate, 16) || !aligned(dw_up, 16)) return FP8BSQ_EALIGN;
-    if (f > kMaxFeatures || k >= kMaxDim) return FP8BSQ_ERANGE;
+    if (!ffn_sizes_ok(1, f, k)) return FP8BSQ_ERANGE;
     // no tokens: the product over an empty contraction
-    return launch_status(fp8bsq::launch_weight_grad(nullptr, nullptr, nullptr, nullptr, dw_gate, dw_up, out_bf16, 0,
-                                                    f, k, st));
+    return launch_status(fp8bsq::launch_gated_ffn_backward(nullptr, nullptr, nullptr, nullptr, in_bf16, nullptr,
+                                                           nullptr, nullptr, nullptr, nullptr, dw_gate, dw_up,
+                                                           out_bf16, 0, f, k, nullptr, st));
   }
   if (!dx && !dw_gate) return FP8BSQ_OK;
   if (!dh || !g || !u || !workspace || (dx && (!w_gate || !w_gate_s || !w_up || !w_up_s)) || (dw_gate && !x))
@@ -119,29 +81,10 @@ int fp8_gated_ffn_backward(const void *dh, const void *x, const void *g, const v
       !aligned(w_up, 16) || !aligned(w_gate_s, 4) || !aligned(w_up_s, 4) || !aligned(dx, 4) ||
       !aligned(dw_gate, 16) || !aligned(dw_up, 16) || !aligned(workspace, 256))
     return FP8BSQ_EALIGN;
-  if (!ffn_sizes_ok(m, f, k) || f > kMaxFeatures) return FP8BSQ_ERANGE;
-  const BackwardSpace ws(m, f, k);
-  if (workspace_bytes < ws.bytes) return FP8BSQ_ESCRATCH;
-  uint8_t *base = (uint8_t *)workspace;
-  uint8_t *rq = base + ws.rq, *cq = base + ws.cq, *ce = base + ws.ce;
-  float *rs = (float *)(base + ws.rs);
-  int rc = launch_status(fp8bsq::launch_ffn_grad_quant(dh, g, u, in_bf16, m, f, dx ? rq : nullptr, rs,
-                                                       dw_gate ? cq : nullptr, ce, st));
-  if (rc != FP8BSQ_OK) return rc;
-  if (dx) {
-    uint8_t *wt = base + ws.wt;
-    float *wt_s = (float *)(base + ws.wt_s);
-    rc = launch_status(fp8bsq::launch_weights_transpose(w_gate, w_gate_s, w_up, w_up_s, f, k, wt, wt_s, st));
-    if (rc != FP8BSQ_OK) return rc;
-    rc = fp8_block_gemm_split(rq, rs, wt, wt_s, dx, out_dtype, m, k, 2 * f, FP8BSQ_SCALE_UE8M0,
-                              ws.split_bytes ? base + ws.split : nullptr, ws.split_bytes, hip_stream);
-    if (rc != FP8BSQ_OK) return rc;
-  }
-  if (!dw_gate) return FP8BSQ_OK;
-  uint8_t *xq = base + ws.xq, *xe = base + ws.xe;
-  rc = launch_status(fp8bsq::launch_token_quant(x, in_bf16, m, k, xq, xe, st));
-  if (rc != FP8BSQ_OK) return rc;
-  return launch_status(fp8bsq::launch_weight_grad(cq, ce, xq, xe, dw_gate, dw_up, out_bf16, m, f, k, st));
+  if (!ffn_sizes_ok(m, f, k)) return FP8BSQ_ERANGE;
+  if (workspace_bytes < fp8bsq::backward_space(m, f, k).bytes) return FP8BSQ_ESCRATCH;
+  return launch_status(fp8bsq::launch_gated_ffn_backward(dh, x, g, u, in_bf16, w_gate, w_gate_s, w_up, w_up_s, dx,
+                                                         dw_gate, dw_up, out_bf16, m, f, k, workspace, st));
 }
 
 int fp4_weight_quant(const void *w, int w_dtype, int64_t n, int64_t k, uint8_t *q, uint8_t *s, void *hip_stream) {

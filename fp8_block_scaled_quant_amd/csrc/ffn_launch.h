@@ -9,43 +9,40 @@
 
 namespace fp8bsq {
 
-// h = silu(g) * u with g, u [m, f] the block-scaled products of the codes a
-// [m, k] (scales a_s; a_s_pow2: all powers of two) and the weights wg, wu
-// [f, k].  g_out, u_out: both null, or both receive g and u.
-hipError_t launch_gated_gemm(const uint8_t *a, const float *a_s, const uint8_t *wg, const float *wg_s,
-                             const uint8_t *wu, const float *wu_s, void *h, void *g_out, void *u_out,
-                             bool a_s_pow2, bool out_bf16, int64_t m, int64_t f, int64_t k,
-                             hipStream_t stream);
+// Where the pieces of a feed-forward call's workspace start, each 256-byte
+// aligned, and its size.
+struct FfnSpace {
+  size_t bytes = 0;
+  size_t a = 0, a_s = 0;          // columns operand of the (input) product, its scales
+  size_t cq = 0, cs = 0;          // backward: (dg | du)^T quantized along the tokens
+  size_t xq = 0, xs = 0;          // backward: x^T quantized along the tokens
+  size_t partials = 0;            // of a split product
+  size_t add(int64_t n) {
+    const size_t at = bytes;
+    bytes += ((size_t)n + 255) / 256 * 256;
+    return at;
+  }
+};
 
-// Columns of the quantized-along-tokens operands: m rounded up to whole blocks.
+// Tokens rounded up to whole blocks of 128, and rows to the widest tile (what a
+// scale row's stride allows for).
 inline int64_t tokens_padded(int64_t m) { return (m + 127) / 128 * 128; }
-// Bytes of one operand's token-block exponents: a 4-byte word per row and four
-// token blocks.
-inline int64_t token_exp_bytes(int64_t rows, int64_t m) { return (tokens_padded(m) / 128 + 3) / 4 * rows * 4; }
+inline int64_t rows_padded(int64_t rows) { return (rows + 255) / 256 * 256; }
 
-// From dh, g, u [m, f]: dg and du, quantized twice.  Along the features: codes
-// rq [m, 2 f] (dg, then du) with scales rs [m, 2 f / 128].  Along the tokens,
-// transposed: codes cq [2 f, tokens_padded(m)] with exponents ce.  Either pair
-// may be null.
-hipError_t launch_ffn_grad_quant(const void *dh, const void *g, const void *u, bool in_bf16, int64_t m,
-                                 int64_t f, uint8_t *rq, float *rs, uint8_t *cq, uint8_t *ce,
-                                 hipStream_t stream);
+// h = silu(g) * u; g_out, u_out: both null, or both receive g and u.
+// workspace: gated_space(m, f, k).bytes.
+FfnSpace gated_space(int64_t m, int64_t f, int64_t k);
+hipError_t launch_gated_ffn(const void *x, bool x_bf16, bool ue8m0, const uint8_t *wg, const float *wg_s,
+                            const uint8_t *wu, const float *wu_s, void *h, void *g_out, void *u_out, bool out_bf16,
+                            int64_t m, int64_t f, int64_t k, void *workspace, hipStream_t stream);
 
-// x [m, k] quantized along the tokens, transposed: cq [k, tokens_padded(m)], ce.
-hipError_t launch_token_quant(const void *x, bool x_bf16, int64_t m, int64_t k, uint8_t *cq, uint8_t *ce,
-                              hipStream_t stream);
-
-// Both weights' codes and scales transposed side by side: wt [k, 2 f],
-// wt_s [k / 128, 2 f / 128].
-hipError_t launch_weights_transpose(const uint8_t *wg, const float *wg_s, const uint8_t *wu,
-                                    const float *wu_s, int64_t f, int64_t k, uint8_t *wt, float *wt_s,
-                                    hipStream_t stream);
-
-// dw [2 f, k] = dgu^T x from the token-quantized operands; rows below f go to
-// dwg, the others to dwu.
-hipError_t launch_weight_grad(const uint8_t *dq, const uint8_t *de, const uint8_t *xq, const uint8_t *xe,
-                              void *dwg, void *dwu, bool out_bf16, int64_t m, int64_t f, int64_t k,
-                              hipStream_t stream);
+// dx, or dwg and dwu, may be null; with m = 0 only the weights' (zero)
+// gradients are written.  workspace: backward_space(m, f, k).bytes.
+FfnSpace backward_space(int64_t m, int64_t f, int64_t k);
+hipError_t launch_gated_ffn_backward(const void *dh, const void *x, const void *g, const void *u, bool in_bf16,
+                                     const uint8_t *wg, const float *wg_s, const uint8_t *wu, const float *wu_s,
+                                     void *dx, void *dwg, void *dwu, bool out_bf16, int64_t m, int64_t f, int64_t k,
+                                     void *workspace, hipStream_t stream);
 
 // w [n, k] -> codes q [n, k / 2] and E8M0 scales s [n, k / 32].
 hipError_t launch_fp4_weight_quant(const void *w, bool w_bf16, int64_t n, int64_t k, uint8_t *q, uint8_t *s,
