@@ -429,12 +429,12 @@ __device__ __forceinline__ void mid_finish(const TileArgs &p, int ta, int tb, in
 }
 
 // kMx: the columns' scales are powers of two and go into the MFMA.
+// Workgroup `block` of the `total` that the product takes.
 template <TileMode kMode, bool kMx, bool kBf16Out>
-__global__ __launch_bounds__(kMidThreads) void e4m3_mid_kernel(const TileArgs p) {
+__device__ __forceinline__ void mid_tile(const TileArgs &p, int block, int total, MidSlot *ring) {
   static_assert(kMode == TileMode::kGated || kMx, "gradient scales are powers of two");
   constexpr bool kGatedMode = kMode == TileMode::kGated, kInputMode = kMode == TileMode::kInput;
   constexpr bool kWeightMode = kMode == TileMode::kWeight;
-  __shared__ __attribute__((aligned(1024))) MidSlot ring[kMidSlots];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fq = lane >> 4, dr = lane >> 3, ds = lane & 7;
@@ -442,8 +442,8 @@ __global__ __launch_bounds__(kMidThreads) void e4m3_mid_kernel(const TileArgs p)
 
   // XCD x (workgroups are dealt to the eight round-robin) takes a contiguous
   // share of the order part, row tile, column tile: neighbours share weights
-  const int total = gridDim.x, xcd = blockIdx.x % 8;
-  const int lin = xcd * (total / 8) + min(xcd, total % 8) + blockIdx.x / 8;
+  const int xcd = block % 8;
+  const int lin = xcd * (total / 8) + min(xcd, total % 8) + block / 8;
   const int ta = lin % p.tiles_a, tb = lin / p.tiles_a % p.tiles_b, part = lin / (p.tiles_a * p.tiles_b);
   const int per = (p.nkb + p.parts - 1) / p.parts;
   const int kb0 = min(p.nkb, part * per), kb1 = min(p.nkb, kb0 + per);
@@ -623,12 +623,18 @@ __global__ __launch_bounds__(kMidThreads) void e4m3_mid_kernel(const TileArgs p)
   }
 }
 
-// Adds a tile's partials in part order: workgroup (tile, i) the column tiles i of
-// the tile's four waves.
+template <TileMode kMode, bool kMx, bool kBf16Out>
+__global__ __launch_bounds__(kMidThreads) void e4m3_mid_kernel(const TileArgs p) {
+  __shared__ __attribute__((aligned(1024))) MidSlot ring[kMidSlots];
+  mid_tile<kMode, kMx, kBf16Out>(p, blockIdx.x, gridDim.x, ring);
+}
+
+// Adds a tile's partials in part order: block 4 tile + i the column tiles i of
+// the tile's four waves (256 threads).
 template <TileMode kMode, bool kBf16Out>
-__global__ __launch_bounds__(256) void e4m3_reduce_kernel(const TileArgs p) {
+__device__ __forceinline__ void mid_reduce(const TileArgs &p, int block) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int tile = blockIdx.x >> 2, i = blockIdx.x & 3;
+  const int tile = block >> 2, i = block & 3;
   f32x4 acc[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = *(const f32x4 *)(mid_partial(p, tile, 0, wave, i, lane) + j * 256);
@@ -639,12 +645,23 @@ __global__ __launch_bounds__(256) void e4m3_reduce_kernel(const TileArgs p) {
   mid_finish<kMode, kBf16Out>(p, tile % p.tiles_a, tile / p.tiles_a, wave, i, lane, acc);
 }
 
+template <TileMode kMode, bool kBf16Out>
+__global__ __launch_bounds__(256) void e4m3_reduce_kernel(const TileArgs p) {
+  mid_reduce<kMode, kBf16Out>(p, blockIdx.x);
+}
+
 // How a product of `nkb` blocks is launched: 256 x 256 tiles, or 128 x 128
 // tiles with the contraction in `parts`.
 struct TilePlan {
   bool big = true;
   int tiles_a = 0, tiles_b = 0, parts = 1;
   size_t partial_bytes = 0;
+
+  void fill(TileArgs &a) const {
+    a.tiles_a = tiles_a;
+    a.tiles_b = tiles_b;
+    a.parts = parts;
+  }
 };
 
 // The cheaper of the two by their time per CU: a block of a 256 x 256 tile takes
@@ -685,9 +702,7 @@ inline TilePlan tile_plan(int64_t cols, int64_t rows, int row_tile, int nkb, int
 template <TileMode kMode, bool kMx>
 inline hipError_t launch_tiles(const TilePlan &plan, TileArgs a, bool out_bf16, int cus, hipStream_t stream) {
   if (cus <= 0) cus = 256;
-  a.tiles_a = plan.tiles_a;
-  a.tiles_b = plan.tiles_b;
-  a.parts = plan.parts;
+  plan.fill(a);
   const int64_t tiles = (int64_t)plan.tiles_a * plan.tiles_b;
   if (plan.big) {
     const dim3 grid((unsigned)(tiles < cus ? tiles : cus)), block(kBigThreads);

@@ -23,12 +23,13 @@ namespace fp8bsq {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Quantizers.  A workgroup of 256 threads owns a 128 x 128 tile; lane l of
-// wave w holds rows 8 (4 w + l / 16) .. + 7 and columns 8 (l % 16) .. + 7, so
-// loads cover 256-byte row segments, a row's amax is a DPP reduction over 16
-// lanes, and a column's eight rows pack into one 8-byte piece of the
-// transposed tile, which goes through LDS to whole-line stores.
+// Quantizers.  A workgroup of 512 threads owns a 128 x 128 tile; lane l of wave
+// w holds rows 4 (4 w + l / 16) .. + 3 and columns 8 (l % 16) .. + 7, so loads
+// cover 256-byte row segments, a row's amax is a DPP reduction over 16 lanes,
+// and a column's four rows pack into one 4-byte piece of the transposed tile,
+// which goes through LDS to whole-line stores.
 // ---------------------------------------------------------------------------
+constexpr int kQuantThreads = 512, kQuantWaves = kQuantThreads / 64, kLaneRows = 4;
 
 template <bool kBf16>
 __device__ __forceinline__ void load8(const void *p, int64_t idx, bool live, float (&v)[8]) {
@@ -58,58 +59,61 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 }
 
 struct TokenTile {
-  uint8_t codes[128 * 128];      // [column][token], 8-byte pieces swizzled by the column
-  uint32_t colmax[4][128];       // per wave
+  uint8_t codes[128 * 128];               // [column][token], 16-byte pieces swizzled by the column
+  uint32_t colmax[kQuantWaves][128];
 };
 
-// Quantize a tile's values v [8 rows][8 columns] along the rows (tokens) and
+// Quantize a tile's values v [4 rows][8 columns] along the rows (tokens) and
 // write it transposed: codes to out [row0 + column][mpad] at token m0, the
 // scales to scales[row0 + column].  Every thread of the workgroup takes part.
-__device__ __forceinline__ void store_tokens(const float (&v)[8][8], TokenTile &sm, uint8_t *__restrict__ out,
+__device__ __forceinline__ void store_tokens(const float (&v)[kLaneRows][8], TokenTile &sm, uint8_t *__restrict__ out,
                                              float *__restrict__ scales, int64_t row0, int64_t m0, int64_t mpad) {
   const int t = threadIdx.x, wave = t >> 6, lane = t & 63, grp = lane >> 4, sub = lane & 15;
   uint32_t top[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    top[c] = 0;
-#pragma unroll
-    for (int r = 0; r < 8; ++r) top[c] = max(top[c], abs_bits(v[r][c]));
+    top[c] = max(max(abs_bits(v[0][c]), abs_bits(v[1][c])), max(abs_bits(v[2][c]), abs_bits(v[3][c])));
     top[c] = max(top[c], (uint32_t)__shfl_xor((int)top[c], 16));
     top[c] = max(top[c], (uint32_t)__shfl_xor((int)top[c], 32));
   }
-  if (grp == 0)
-#pragma unroll
-    for (int c = 0; c < 8; ++c) sm.colmax[wave][8 * sub + c] = top[c];
+  if (grp == 0) {
+    *(u32x4 *)&sm.colmax[wave][8 * sub] = u32x4{top[0], top[1], top[2], top[3]};
+    *(u32x4 *)&sm.colmax[wave][8 * sub + 4] = u32x4{top[4], top[5], top[6], top[7]};
+  }
   __syncthreads();
+  u32x4 lo = *(const u32x4 *)&sm.colmax[0][8 * sub], hi = *(const u32x4 *)&sm.colmax[0][8 * sub + 4];
+#pragma unroll
+  for (int w = 1; w < kQuantWaves; ++w) {
+    lo = __builtin_elementwise_max(lo, *(const u32x4 *)&sm.colmax[w][8 * sub]);
+    hi = __builtin_elementwise_max(hi, *(const u32x4 *)&sm.colmax[w][8 * sub + 4]);
+  }
+  const int piece = wave;   // 16 tokens
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const int col = 8 * sub + c;
-    const uint32_t e = e4m3_scale_byte(max(max(sm.colmax[0][col], sm.colmax[1][col]),
-                                           max(sm.colmax[2][col], sm.colmax[3][col])));
+    const uint32_t e = e4m3_scale_byte(c < 4 ? lo[c & 3] : hi[c & 3]);
     const float inv = pow2_inverse(e);
-    u32x2 q;
-    q.x = codes4(v[0][c] * inv, v[1][c] * inv, v[2][c] * inv, v[3][c] * inv);
-    q.y = codes4(v[4][c] * inv, v[5][c] * inv, v[6][c] * inv, v[7][c] * inv);
-    *(u32x2 *)&sm.codes[col * 128 + (((4 * wave + grp) ^ sub) << 3)] = q;
+    *(uint32_t *)&sm.codes[col * 128 + ((piece ^ (sub & 7)) << 4) + 4 * grp] =
+        codes4(v[0][c] * inv, v[1][c] * inv, v[2][c] * inv, v[3][c] * inv);
     if (wave == 0 && grp == 0) scales[row0 + col] = pow2_scale(e);
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int idx = i * 256 + t, col = idx >> 3, j = idx & 7, s = (col >> 3) & 15;
-    const u32x2 lo = *(const u32x2 *)&sm.codes[col * 128 + (((2 * j) ^ s) << 3)];
-    const u32x2 hi = *(const u32x2 *)&sm.codes[col * 128 + (((2 * j + 1) ^ s) << 3)];
-    *(u32x4 *)(out + (row0 + col) * mpad + m0 + 16 * j) = u32x4{lo.x, lo.y, hi.x, hi.y};
+  for (int i = 0; i < 128 * 8 / kQuantThreads; ++i) {
+    const int idx = i * kQuantThreads + t, col = idx >> 3, j = idx & 7;
+    *(u32x4 *)(out + (row0 + col) * mpad + m0 + 16 * j) =
+        *(const u32x4 *)&sm.codes[col * 128 + ((j ^ ((col >> 3) & 7)) << 4)];
   }
   __syncthreads();   // the tile may be reused
 }
 
-// Quantize each row's 128 columns: codes to out + row * ld, scale to scales[row].
-__device__ __forceinline__ void store_rows(const float (&v)[8][8], uint8_t *__restrict__ out, int64_t ld,
+// Quantize each row's 128 columns: codes to out + row * ld (the lane's eight
+// columns), scale to scales[row].
+__device__ __forceinline__ void store_rows(const float (&v)[kLaneRows][8], uint8_t *__restrict__ out, int64_t ld,
                                            float *__restrict__ scales, int64_t row0, int64_t m) {
   const int sub = threadIdx.x & 15;
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
+  for (int r = 0; r < kLaneRows; ++r) {
     uint32_t top = 0;
 #pragma unroll
     for (int c = 0; c < 8; ++c) top = max(top, abs_bits(v[r][c]));
@@ -119,62 +123,124 @@ __device__ __forceinline__ void store_rows(const float (&v)[8][8], uint8_t *__re
       u32x2 q;
       q.x = codes4(v[r][0] * inv, v[r][1] * inv, v[r][2] * inv, v[r][3] * inv);
       q.y = codes4(v[r][4] * inv, v[r][5] * inv, v[r][6] * inv, v[r][7] * inv);
-      *(u32x2 *)(out + (row0 + r) * ld + 8 * sub) = q;
+      *(u32x2 *)(out + (row0 + r) * ld) = q;
       if (sub == 0) scales[row0 + r] = pow2_scale(e);
     }
   }
 }
 
+struct QuantArgs {
+  const void *dh, *g, *u, *x;
+  int64_t m, f, k, mpad;
+  uint8_t *rq;   // [m][2 f] codes along the features, or null
+  float *rs;     // [2 f / 128][rs_stride]
+  int64_t rs_stride;
+  uint8_t *cq;   // [2 f][mpad] codes along the tokens, or null
+  float *cs;     // [mpad / 128][cs_stride]
+  int64_t cs_stride;
+  uint8_t *xq;   // [k][mpad], with cq
+  float *xs;     // [mpad / 128][k]
+  int grad_tiles, split;
+};
+
+// Everything that the products read, in one launch: workgroups below
+// grad_tiles * split quantize a tile of dg and du, the others a tile of x.  With
+// fewer tiles than CUs the tile's four results (dg or du, along the features or
+// the tokens) go to a workgroup each (split = 4), which all form the gradient
+// anew: 333 x 1024 took 15 us in one piece, its arithmetic on 24 CUs.
 template <bool kBf16>
-__global__ __launch_bounds__(256) void ffn_grad_quant_kernel(
-    const void *__restrict__ dh, const void *__restrict__ g, const void *__restrict__ u, int64_t m, int64_t f,
-    int64_t mpad, uint8_t *__restrict__ rq, float *__restrict__ rs, int64_t rs_stride, uint8_t *__restrict__ cq,
-    float *__restrict__ cs, int64_t cs_stride) {
+__global__ __launch_bounds__(kQuantThreads) void ffn_quant_kernel(const QuantArgs p) {
   __shared__ TokenTile sm;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t f0 = (int64_t)blockIdx.x * kBlock, m0 = (int64_t)blockIdx.y * kBlock;
-  const int64_t row0 = m0 + 8 * (4 * wave + (lane >> 4)), col0 = f0 + 8 * (lane & 15);
-  float dg[8][8], du[8][8];
+  const int lane_row = kLaneRows * (4 * wave + (lane >> 4)), lane_col = 8 * (lane & 15);
+  if ((int)blockIdx.x >= p.grad_tiles * p.split) {
+    const int tile = blockIdx.x - p.grad_tiles * p.split, across = (int)(p.k / kBlock);
+    const int64_t m0 = (int64_t)(tile / across) * kBlock, k0 = (int64_t)(tile % across) * kBlock;
+    float v[kLaneRows][8];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const bool live = row0 + r < m;
-    const int64_t idx = (row0 + r) * f + col0;
+    for (int r = 0; r < kLaneRows; ++r) {
+      const int64_t row = m0 + lane_row + r;
+      load8<kBf16>(p.x, row * p.k + k0 + lane_col, row < p.m, v[r]);
+    }
+    store_tokens(v, sm, p.xq, p.xs + m0 / kBlock * p.k, k0, m0, p.mpad);
+    return;
+  }
+  const int tile = blockIdx.x / p.split, piece = blockIdx.x % p.split, across = (int)(p.f / kBlock);
+  const int64_t m0 = (int64_t)(tile / across) * kBlock, f0 = (int64_t)(tile % across) * kBlock;
+  const bool all = p.split == 1;
+  const bool rows = p.rq && (all || piece < 2), tokens = p.cq && (all || piece >= 2);
+  if (!rows && !tokens) return;
+  const int64_t row0 = m0 + lane_row;
+  float dg[kLaneRows][8], du[kLaneRows][8];
+#pragma unroll
+  for (int r = 0; r < kLaneRows; ++r) {
+    const bool live = row0 + r < p.m;
+    const int64_t idx = (row0 + r) * p.f + f0 + lane_col;
     float hv[8], gv[8], uv[8];
-    load8<kBf16>(dh, idx, live, hv);
-    load8<kBf16>(g, idx, live, gv);
-    load8<kBf16>(u, idx, live, uv);
+    load8<kBf16>(p.dh, idx, live, hv);
+    load8<kBf16>(p.g, idx, live, gv);
+    load8<kBf16>(p.u, idx, live, uv);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float s = 1.0f / (1.0f + __expf(-gv[c]));
+      // the reciprocal instruction is within one ulp; exp overflows to infinity
+      // for g below -88, where the sigmoid is 0 to fp32's precision
+      const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-gv[c]));
       du[r][c] = hv[c] * (gv[c] * s);
       dg[r][c] = hv[c] * uv[c] * (s * __builtin_fmaf(gv[c], 1.0f - s, 1.0f));
     }
   }
-  if (rq) {
-    const int64_t nfb = f / kBlock;
-    float *s = rs + blockIdx.x * rs_stride;
-    store_rows(dg, rq + f0, 2 * f, s, row0, m);
-    store_rows(du, rq + f + f0, 2 * f, s + nfb * rs_stride, row0, m);
+  const bool gate = all || (piece & 1) == 0, up = all || (piece & 1) == 1;
+  if (rows) {
+    float *s = p.rs + f0 / kBlock * p.rs_stride;
+    if (gate) store_rows(dg, p.rq + f0 + lane_col, 2 * p.f, s, row0, p.m);
+    if (up) store_rows(du, p.rq + p.f + f0 + lane_col, 2 * p.f, s + p.f / kBlock * p.rs_stride, row0, p.m);
   }
-  if (cq) {
-    float *s = cs + blockIdx.y * cs_stride;
-    store_tokens(dg, sm, cq, s, f0, m0, mpad);
-    store_tokens(du, sm, cq, s, f + f0, m0, mpad);
+  if (tokens) {
+    float *s = p.cs + m0 / kBlock * p.cs_stride;
+    if (gate) store_tokens(dg, sm, p.cq, s, f0, m0, p.mpad);
+    if (up) store_tokens(du, sm, p.cq, s, p.f + f0, m0, p.mpad);
   }
 }
 
-template <bool kBf16>
-__global__ __launch_bounds__(256) void token_quant_kernel(const void *__restrict__ x, int64_t m, int64_t k,
-                                                          int64_t mpad, uint8_t *__restrict__ cq,
-                                                          float *__restrict__ cs) {
-  __shared__ TokenTile sm;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t k0 = (int64_t)blockIdx.x * kBlock, m0 = (int64_t)blockIdx.y * kBlock;
-  const int64_t row0 = m0 + 8 * (4 * wave + (lane >> 4)), col0 = k0 + 8 * (lane & 15);
-  float v[8][8];
-#pragma unroll
-  for (int r = 0; r < 8; ++r) load8<kBf16>(x, (row0 + r) * k + col0, row0 + r < m, v[r]);
-  store_tokens(v, sm, cq, cs + blockIdx.y * k, k0, m0, mpad);
+// dx and dW in one launch, where both are too small to fill the GPU: the first
+// `first` workgroups are dx's.
+template <bool kBf16Out>
+__global__ __launch_bounds__(kMidThreads) void mid_pair_kernel(const TileArgs in, const TileArgs wt, int first) {
+  __shared__ __attribute__((aligned(1024))) MidSlot ring[kMidSlots];
+  if ((int)blockIdx.x < first)
+    mid_tile<TileMode::kInput, true, kBf16Out>(in, blockIdx.x, first, ring);
+  else
+    mid_tile<TileMode::kWeight, true, kBf16Out>(wt, blockIdx.x - first, gridDim.x - first, ring);
+}
+
+template <bool kBf16Out>
+__global__ __launch_bounds__(256) void reduce_pair_kernel(const TileArgs in, const TileArgs wt, int first) {
+  if ((int)blockIdx.x < first)
+    mid_reduce<TileMode::kInput, kBf16Out>(in, blockIdx.x);
+  else
+    mid_reduce<TileMode::kWeight, kBf16Out>(wt, blockIdx.x - first);
+}
+
+hipError_t launch_mid_pair(const TilePlan &in, TileArgs pi, const TilePlan &wt, TileArgs pw, bool out_bf16,
+                           hipStream_t stream) {
+  in.fill(pi);
+  wt.fill(pw);
+  const int first = in.tiles_a * in.tiles_b * in.parts;
+  const dim3 grid((unsigned)(first + wt.tiles_a * wt.tiles_b * wt.parts)), block(kMidThreads);
+  if (out_bf16)
+    hipLaunchKernelGGL(mid_pair_kernel<true>, grid, block, 0, stream, pi, pw, first);
+  else
+    hipLaunchKernelGGL(mid_pair_kernel<false>, grid, block, 0, stream, pi, pw, first);
+  const int rin = in.parts > 1 ? in.tiles_a * in.tiles_b * 4 : 0, rwt = wt.parts > 1 ? wt.tiles_a * wt.tiles_b * 4 : 0;
+  if (rin + rwt > 0) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (out_bf16)
+      hipLaunchKernelGGL(reduce_pair_kernel<true>, dim3((unsigned)(rin + rwt)), dim3(256), 0, stream, pi, pw, rin);
+    else
+      hipLaunchKernelGGL(reduce_pair_kernel<false>, dim3((unsigned)(rin + rwt)), dim3(256), 0, stream, pi, pw, rin);
+  }
+  return hipGetLastError();
 }
 
 TilePlan input_plan(int64_t m, int64_t f, int64_t k) {
@@ -196,8 +262,7 @@ FfnSpace backward_space(int64_t m, int64_t f, int64_t k) {
   s.cs = s.add((mpad / kBlock) * rows_padded(2 * f) * 4);
   s.xq = s.add(k * mpad);
   s.xs = s.add((mpad / kBlock) * k * 4);
-  // one after the other on the stream, the two products share the partials
-  s.partials = s.add((int64_t)(in.partial_bytes > wt.partial_bytes ? in.partial_bytes : wt.partial_bytes));
+  s.partials = s.add((int64_t)(in.partial_bytes + wt.partial_bytes));
   return s;
 }
 
@@ -211,67 +276,71 @@ hipError_t launch_gated_ffn_backward(const void *dh, const void *x, const void *
   const int cus = current_device_cus();
   uint8_t *base = (uint8_t *)workspace;
   float *partials = (float *)(base + ws.partials);
-  hipError_t e = hipSuccess;
   if (m > 0) {
-    const dim3 grid((unsigned)(f / kBlock), (unsigned)(mpad / kBlock));
-#define FP8BSQ_GRAD_QUANT(BF)                                                                                   \
-  hipLaunchKernelGGL(ffn_grad_quant_kernel<BF>, grid, dim3(256), 0, stream, dh, g, u, m, f, mpad,               \
-                     dx ? base + ws.a : nullptr, (float *)(base + ws.a_s), rows_padded(m),                      \
-                     dwg ? base + ws.cq : nullptr, (float *)(base + ws.cs), rows_padded(2 * f))
-    if (in_bf16) FP8BSQ_GRAD_QUANT(true); else FP8BSQ_GRAD_QUANT(false);
-#undef FP8BSQ_GRAD_QUANT
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (dwg) {
-      const dim3 xgrid((unsigned)(k / kBlock), (unsigned)(mpad / kBlock));
-      if (in_bf16)
-        hipLaunchKernelGGL(token_quant_kernel<true>, xgrid, dim3(256), 0, stream, x, m, k, mpad, base + ws.xq,
-                           (float *)(base + ws.xs));
-      else
-        hipLaunchKernelGGL(token_quant_kernel<false>, xgrid, dim3(256), 0, stream, x, m, k, mpad, base + ws.xq,
-                           (float *)(base + ws.xs));
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-  }
-  if (dx && m > 0) {
-    TileArgs p = {};
-    p.a = base + ws.a;
-    p.a_s = (const float *)(base + ws.a_s);
-    p.b0 = wg;
-    p.b1 = wu;
-    p.b0_s = wg_s;
-    p.b1_s = wu_s;
-    p.out0 = dx;
-    p.partials = partials;
-    p.rows_a = m;
-    p.rows_b = k;
-    p.lda = 2 * f;
-    p.ldb = k;
-    p.a_stride = rows_padded(m);
-    p.nkb = (int)(2 * f / kBlock);
-    p.half = (int)(f / kBlock);
-    e = launch_tiles<TileMode::kInput, true>(in, p, out_bf16, cus, stream);
+    QuantArgs q = {};
+    q.dh = dh;
+    q.g = g;
+    q.u = u;
+    q.x = x;
+    q.m = m;
+    q.f = f;
+    q.k = k;
+    q.mpad = mpad;
+    q.rq = dx ? base + ws.a : nullptr;
+    q.rs = (float *)(base + ws.a_s);
+    q.rs_stride = rows_padded(m);
+    q.cq = dwg ? base + ws.cq : nullptr;
+    q.cs = (float *)(base + ws.cs);
+    q.cs_stride = rows_padded(2 * f);
+    q.xq = base + ws.xq;
+    q.xs = (float *)(base + ws.xs);
+    const int64_t grad_tiles = (f / kBlock) * (mpad / kBlock), x_tiles = dwg ? (k / kBlock) * (mpad / kBlock) : 0;
+    q.grad_tiles = (int)grad_tiles;
+    q.split = grad_tiles < (cus > 0 ? cus : 256) ? 4 : 1;
+    const dim3 grid((unsigned)(grad_tiles * q.split + x_tiles));
+    if (in_bf16)
+      hipLaunchKernelGGL(ffn_quant_kernel<true>, grid, dim3(kQuantThreads), 0, stream, q);
+    else
+      hipLaunchKernelGGL(ffn_quant_kernel<false>, grid, dim3(kQuantThreads), 0, stream, q);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (dwg) {
-    TileArgs p = {};
-    p.a = base + ws.cq;
-    p.a_s = (const float *)(base + ws.cs);
-    p.b0 = base + ws.xq;
-    p.b0_s = (const float *)(base + ws.xs);
-    p.out0 = dwg;
-    p.out1 = dwu;
-    p.partials = partials;
-    p.rows_a = 2 * f;
-    p.rows_b = k;
-    p.lda = p.ldb = mpad;
-    p.a_stride = rows_padded(2 * f);
-    p.b_stride = k;
-    p.nkb = (int)(mpad / kBlock);
-    e = launch_tiles<TileMode::kWeight, true>(wt, p, out_bf16, cus, stream);
+  TileArgs pi = {}, pw = {};
+  pi.a = base + ws.a;
+  pi.a_s = (const float *)(base + ws.a_s);
+  pi.b0 = wg;
+  pi.b1 = wu;
+  pi.b0_s = wg_s;
+  pi.b1_s = wu_s;
+  pi.out0 = dx;
+  pi.partials = (float *)(base + ws.partials);
+  pi.rows_a = m;
+  pi.rows_b = k;
+  pi.lda = 2 * f;
+  pi.ldb = k;
+  pi.a_stride = rows_padded(m);
+  pi.nkb = (int)(2 * f / kBlock);
+  pi.half = (int)(f / kBlock);
+  pw.a = base + ws.cq;
+  pw.a_s = (const float *)(base + ws.cs);
+  pw.b0 = base + ws.xq;
+  pw.b0_s = (const float *)(base + ws.xs);
+  pw.out0 = dwg;
+  pw.out1 = dwu;
+  pw.partials = (float *)(base + ws.partials) + in.partial_bytes / sizeof(float);
+  pw.rows_a = 2 * f;
+  pw.rows_b = k;
+  pw.lda = pw.ldb = mpad;
+  pw.a_stride = rows_padded(2 * f);
+  pw.b_stride = k;
+  pw.nkb = (int)(mpad / kBlock);
+  const bool want_dx = dx && m > 0;
+  if (want_dx && dwg && !in.big && !wt.big) return launch_mid_pair(in, pi, wt, pw, out_bf16, stream);
+  if (want_dx) {
+    const hipError_t e = launch_tiles<TileMode::kInput, true>(in, pi, out_bf16, cus, stream);
+    if (e != hipSuccess) return e;
   }
-  return e;
+  return dwg ? launch_tiles<TileMode::kWeight, true>(wt, pw, out_bf16, cus, stream) : hipSuccess;
 }
 
 }  // namespace fp8bsq
