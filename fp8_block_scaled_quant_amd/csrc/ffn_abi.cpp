@@ -12,6 +12,7 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t)1 << 31;         // per-dimension limit of the launch grids
 constexpr int64_t kMaxRows = (int64_t)65535 * 16;     // grid.y limit of the smallest row tile
 constexpr int64_t kMaxFeatures = (int64_t)1 << 21;    // features and K of the feed-forward block
+constexpr int64_t kMaxGemvK = (int64_t)1 << 27;       // 16 rows of codes within 32-bit offsets
 
 bool aligned(const void *p, uintptr_t bytes) { return ((uintptr_t)p % bytes) == 0; }
 bool known_dtype(int d) { return d == FP8BSQ_F32 || d == FP8BSQ_BF16; }
@@ -108,7 +109,7 @@ int fp4_gemv(const void *x, int x_dtype, const uint8_t *q, const uint8_t *s, con
   if (!x || !q || !s || !y) return FP8BSQ_EINVAL;
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(bias, size_of(y_dtype)) || !aligned(y, size_of(y_dtype)))
     return FP8BSQ_EALIGN;
-  if (m > kMaxRows || n >= kMaxDim || k >= kMaxDim) return FP8BSQ_ERANGE;
+  if (m > kMaxRows || n >= kMaxDim || k > kMaxGemvK) return FP8BSQ_ERANGE;
   return launch_status(fp8bsq::launch_fp4_gemv(x, x_dtype == FP8BSQ_BF16, q, s, bias, y, y_dtype == FP8BSQ_BF16, m,
                                                n, k, (hipStream_t)hip_stream));
 }

@@ -1,5 +1,6 @@
 // 4-bit weights for gfx950: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign),
 // two to a byte, and one E8M0 scale byte per 32 weights of a row.
+#include "device_cus.h"
 #include "ffn_launch.h"
 #include "mfma_tile.h"
 #include "pow2_scale.h"
@@ -62,15 +63,22 @@ __global__ __launch_bounds__(256) void fp4_weight_quant_kernel(const void *__res
 // one instruction turns two codes and the scale into two bf16, so the group
 // scales cost nothing in the product and one FP32 accumulator runs through K.
 //
-// MFMA 16x16x32 with the weights as the 16-row operand and up to 16 rows of x
-// as columns.  The order of K inside the operands is free as long as both
-// agree: lane l takes weight row l % 16 and the whole group 4 step + l / 16 --
-// 16 bytes of codes and one scale -- and feeds it to four MFMAs, eight codes
-// each; x's lane reads the same eight k.  The four waves of a workgroup split
-// the steps of 128 k and add their sums in LDS.
+// MFMA 16x16x32 with the weights as the 16-row operand and 16 rows of x as
+// columns.  The order of K inside the operands is free as long as both agree:
+// lane l takes weight row l % 16 and the whole group 4 step + l / 16 -- 16 bytes
+// of codes and one scale -- and feeds it to four MFMAs, eight codes each; x's
+// lane reads the same eight k.
 //
-// fp32 x is split exactly into three bf16 (3 x 8 significand bits), one MFMA
-// each.
+// The weights' bytes bound the product.  A block is 256 k: 128 bytes of codes a
+// row.  Compute waves (`tiles` row tiles of 16, times `parts` that split K) move
+// their own 16 rows, whole lines, by direct global->LDS transfers into a
+// kDepth-slot ring, and wait for nothing else of their own.  Helper waves bring
+// what the weights meet, a step of `blocks` blocks ahead, through registers: the
+// scales, and x as bf16 planes (each value once per workgroup; fp32 x is split
+// exactly into three bf16, 3 x 8 significand bits, one MFMA each).  One barrier
+// per step hands these on; within a step the waves run freely.  (With fragments
+// loaded straight to registers, 64 bytes of a row at a time, and x read by every
+// wave, 18432 x 7168 and one row took 24 us.)
 // ---------------------------------------------------------------------------
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -86,67 +94,286 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) {   //
   return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
-constexpr int kGemvWaves = 4;
+// Eight fp32 as the sum of three bf16 each: the upper 16 bits of what is left.
+__device__ __forceinline__ void split3(float (&r)[8], u32x4 (&parts)[3]) {
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) parts[q][c] = high_halves(__float_as_uint(r[2 * c]), __float_as_uint(r[2 * c + 1]));
+#pragma unroll
+    for (int c = 0; c < 8; ++c) r[c] -= __uint_as_float(__float_as_uint(r[c]) & 0xFFFF0000u);
+  }
+}
 
-template <bool kBf16X, bool kBf16Out>
-__global__ __launch_bounds__(64 * kGemvWaves) void fp4_gemv_kernel(
-    const void *__restrict__ x, const uint8_t *__restrict__ q, const uint8_t *__restrict__ s,
-    const void *__restrict__ bias, void *__restrict__ y, int64_t m, int64_t n, int64_t k) {
-  __shared__ f32x4 sums[kGemvWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lq = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * 16;
-  const int ng = (int)(k / kGroup);
-  const int64_t row = min(n0 + lr, n - 1);
-  const uint8_t *qrow = q + row * (k / 2), *srow = s + row * ng;
-  const bool xlive = m0 + lr < m;
-  const int64_t xrow = (m0 + (xlive ? lr : 0)) * k;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int step = wave; 4 * step < ng; step += kGemvWaves) {
-    const int grp = 4 * step + lq;
-    const bool live = grp < ng;
-    u32x4 codes = {0, 0, 0, 0};
-    float scale = 1.0f;
-    if (live) {
-      codes = *(const u32x4 *)(qrow + (int64_t)grp * 16);
-      scale = pow2_scale(srow[grp]);
-    }
+constexpr int kGemvBlock = 256;        // k per block
+constexpr int kGemvSlot = 16 * 128;    // bytes of codes a wave takes per block
+constexpr int kGemvPieces = 8;         // 8-value pieces of x that a helper lane carries
+constexpr int kGemvBlocksMax = 4;      // blocks per step
+constexpr int kGemvComputeMax = 10, kGemvWavesMax = 16;
+
+struct GemvArgs {
+  const void *x, *bias;
+  const uint8_t *q, *s;
+  void *y;
+  int64_t m, n, k;
+  int tiles, parts, blocks, helpers;
+  bool out_bf16;
+};
+
+template <bool kBf16X, int kMT, int kDepth>
+__global__ __launch_bounds__(64 * kGemvWavesMax) void fp4_gemv_kernel(const GemvArgs p) {
+  constexpr int kPlanes = kBf16X ? 1 : 3;
+  // codes [compute wave][slot][16 x 128]; scales [2][compute wave][block][16 x 8];
+  // x [2][part][block][plane][row][512 bytes]
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int compute = p.tiles * p.parts;
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * kMT);
+  const int rows = (int)min((int64_t)16 * kMT, p.m - m0);
+  const int ng = (int)(p.k / kGroup), nblk = (ng + 7) / 8, per = (nblk + p.parts - 1) / p.parts;
+  const int steps = (per + p.blocks - 1) / p.blocks;
+  const int sslot = compute * p.blocks * 128, xslot = p.parts * p.blocks * kPlanes * rows * 512;
+  uint8_t *scales = lds + compute * kDepth * kGemvSlot;
+  uint8_t *xs = scales + 2 * sslot;
+
+  if (wave >= compute) {
+    const int helper = wave - compute;
+    if (helper == p.helpers) {
+      // scales: eight bytes of (compute wave, block, row)
+      constexpr int kEights = (kGemvComputeMax * kGemvBlocksMax * 16 + 63) / 64;
+      const int pieces = compute * p.blocks * 16;
+      uint64_t v[kEights];
+      int64_t src[kEights];   // of step 0
+      int group[kEights];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const bf16x8 w = fp4_to_bf16(codes[t], scale);
-      const int64_t at = xrow + (int64_t)grp * kGroup + 8 * t;
-      if (kBf16X) {
-        u32x4 xv = {0, 0, 0, 0};
-        if (live && xlive) xv = *(const u32x4 *)((const uint16_t *)x + at);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, xv), acc, 0, 0, 0);
-      } else {
-        f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-        if (live && xlive) {
-          lo = *(const f32x4 *)((const float *)x + at);
-          hi = *(const f32x4 *)((const float *)x + at + 4);
+      for (int i = 0; i < kEights; ++i) {
+        const int idx = i * 64 + lane, w = idx / (p.blocks * 16), b = (idx >> 4) - w * p.blocks;
+        const int64_t row = min(((int64_t)blockIdx.x * p.tiles + w / p.parts) * 16 + (idx & 15), p.n - 1);
+        group[i] = 8 * (w % p.parts * per + b);
+        src[i] = row * ng + group[i];
+      }
+      auto load = [&](int step) {
+#pragma unroll
+        for (int i = 0; i < kEights; ++i) {
+          const int ahead = 8 * step * p.blocks, left = ng - group[i] - ahead;
+          v[i] = 0;
+          if (i * 64 + lane >= pieces || left <= 0) continue;
+          if (src[i] + ahead + 8 <= p.n * ng)   // past the row's end lies the next row's, unused
+            __builtin_memcpy(&v[i], p.s + src[i] + ahead, 8);
+          else
+            for (int c = 0; c < 8 && c < left; ++c) v[i] |= (uint64_t)p.s[src[i] + ahead + c] << (8 * c);
         }
-        float r[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      };
+      auto store = [&](int step) {
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          u32x4 p;
+        for (int i = 0; i < kEights; ++i)
+          if (i * 64 + lane < pieces) *(uint64_t *)(scales + (step & 1) * sslot + (i * 64 + lane) * 8) = v[i];
+      };
+      load(0);
+      store(0);
+      load(1);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      workgroup_barrier();
+      for (int step = 0; step < steps; ++step) {
+        store(step + 1);   // into the buffer of step - 1
+        load(step + 2);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        workgroup_barrier();
+      }
+    } else {
+      // x: eight values of (part, block, row)
+      const int pieces = p.parts * p.blocks * rows * 32, stride = p.helpers * 64;
+      u32x4 v[kGemvPieces][kBf16X ? 1 : 2];
+      int64_t base[kGemvPieces];   // the row's first value
+      int k0[kGemvPieces], dst[kGemvPieces];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) p[c] = high_halves(__float_as_uint(r[2 * c]), __float_as_uint(r[2 * c + 1]));
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, p), acc, 0, 0, 0);
+      for (int i = 0; i < kGemvPieces; ++i) {
+        const int idx = i * stride + helper * 64 + lane, pb = idx / (rows * 32), row = (idx >> 5) - pb * rows;
+        const int part = pb / p.blocks, b = pb - part * p.blocks;
+        base[i] = (m0 + row) * p.k;
+        k0[i] = (part * per + b) * kGemvBlock + 8 * (idx & 31);
+        dst[i] = (pb * kPlanes * rows + row) * 512 + (((idx & 31) ^ (row & 15)) << 4);
+      }
+      auto load = [&](int step) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) r[c] -= __uint_as_float(__float_as_uint(r[c]) & 0xFFFF0000u);
+        for (int i = 0; i < kGemvPieces; ++i) {
+          if (i * stride + helper * 64 + lane >= pieces) continue;
+          // past the end any x will do: the codes it meets are zero
+          const int64_t at = base[i] + min(k0[i] + step * p.blocks * kGemvBlock, (int)p.k - 8);
+          if constexpr (kBf16X) {
+            v[i][0] = *(const u32x4 *)((const uint16_t *)p.x + at);
+          } else {
+            v[i][0] = *(const u32x4 *)((const float *)p.x + at);
+            v[i][1] = *(const u32x4 *)((const float *)p.x + at + 4);
+          }
         }
+      };
+      auto store = [&](int step) {
+        uint8_t *slot = xs + (step & 1) * xslot;
+#pragma unroll
+        for (int i = 0; i < kGemvPieces; ++i) {
+          if (i * stride + helper * 64 + lane >= pieces) continue;
+          if constexpr (kBf16X) {
+            *(u32x4 *)(slot + dst[i]) = v[i][0];
+          } else {
+            float r[8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              r[c] = __uint_as_float(v[i][0][c]);
+              r[4 + c] = __uint_as_float(v[i][1][c]);
+            }
+            u32x4 planes[3];
+            split3(r, planes);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) *(u32x4 *)(slot + dst[i] + q * rows * 512) = planes[q];
+          }
+        }
+      };
+      load(0);
+      store(0);
+      load(1);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      workgroup_barrier();
+      for (int step = 0; step < steps; ++step) {
+        store(step + 1);   // into the slot of step - 1
+        load(step + 2);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        workgroup_barrier();
       }
     }
+    if (p.parts > 1) {   // the compute waves' sums
+      workgroup_barrier();
+      workgroup_barrier();
+    }
+    return;
   }
-  sums[wave][lane] = acc;
-  __syncthreads();
-  if (wave != 0 || !xlive) return;
+
+  const int tile = wave / p.parts, part = wave - tile * p.parts;
+  const int64_t n0 = ((int64_t)blockIdx.x * p.tiles + tile) * 16;
+  const int64_t nc = min(n0, p.n - 1);   // rows past the last re-read it
+  const int lr = lane & 15, lq = lane >> 4, dr = lane >> 3, ds = lane & 7;
+  const int blk0 = part * per, blk1 = min(nblk, blk0 + per);
+  const uint8_t *base = p.q + nc * (p.k / 2);
+  const uint32_t row_off[2] = {(uint32_t)((min(nc + dr, p.n - 1) - nc) * (p.k / 2)),
+                               (uint32_t)((min(nc + 8 + dr, p.n - 1) - nc) * (p.k / 2))};
+  const int chunk[2] = {ds ^ swz(dr), ds ^ swz(8 + dr)};
+  const uint8_t *ring = lds + wave * kDepth * kGemvSlot;
+  const uint32_t lds_ring = lds_addr(ring);
+  auto issue = [&](int j) {   // groups past a row's end re-read its last one; so do blocks past the end
+    const int blk = max(min(blk0 + j, blk1 - 1), 0);
+    const uint32_t slot = lds_ring + (uint32_t)(j % kDepth) * kGemvSlot;
 #pragma unroll
-  for (int w = 1; w < kGemvWaves; ++w) acc += sums[w][lane];
+    for (int i = 0; i < 2; ++i) lds_dma16(base, row_off[i] + (uint32_t)min(8 * blk + chunk[i], ng - 1) * 16, slot + i * 1024);
+  };
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int64_t col = n0 + 4 * lq + e;
-    if (col < n) store_out(y, kBf16Out, (m0 + lr) * n + col, acc[e] + bias_at(bias, kBf16Out, col));
+  for (int d = 0; d < kDepth; ++d) issue(d);
+  f32x4 sum[2][kMT];   // of the even and the odd groups: two chains of MFMAs
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) sum[h][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  workgroup_barrier();
+  for (int step = 0; step < steps; ++step) {
+    const int end = min((step + 1) * p.blocks, blk1 - blk0);
+    for (int j = step * p.blocks; j < end; ++j) {
+      const int b = j - step * p.blocks;
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (kDepth - 1)) : "memory");   // block j landed
+      const uint8_t *slot = ring + j % kDepth * kGemvSlot + lr * 128;
+      u32x4 codes[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) codes[h] = *(const u32x4 *)(slot + (((2 * lq + h) ^ swz(lr)) << 4));
+      const uint32_t sc = *(const uint16_t *)(scales + (step & 1) * sslot + ((wave * p.blocks + b) * 16 + lr) * 8 + 2 * lq);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read: the slot may be refilled
+      issue(j + kDepth);
+      const uint8_t *xb = xs + (step & 1) * xslot + (part * p.blocks + b) * kPlanes * rows * 512;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool live = 8 * (blk0 + j) + 2 * lq + h < ng;
+          const float scale = pow2_scale(live ? (sc >> (8 * h)) & 0xFFu : 127u);
+          const bf16x8 w = fp4_to_bf16(live ? codes[h][t] : 0u, scale);
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt) {
+            const int row = min(16 * mt + lr, rows - 1);   // a column past the last row has no output
+            const uint8_t *at = xb + row * 512 + (((8 * lq + 4 * h + t) ^ (row & 15)) << 4);
+#pragma unroll
+            for (int q = 0; q < kPlanes; ++q)
+              sum[h][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, *(const bf16x8 *)(at + q * rows * 512), sum[h][mt],
+                                                                   0, 0, 0);
+          }
+        }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    workgroup_barrier();
   }
+  f32x4 acc[kMT];
+#pragma unroll
+  for (int mt = 0; mt < kMT; ++mt) acc[mt] = sum[0][mt] + sum[1][mt];
+  wait_dma_all();   // transfers past the end, before LDS is used anew or released
+  if (p.parts > 1) {   // the parts' sums, in part order
+    f32x4 *sums = (f32x4 *)lds;
+    workgroup_barrier();
+    if (part > 0)
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt) sums[(wave * kMT + mt) * 64 + lane] = acc[mt];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    workgroup_barrier();
+    if (part > 0) return;
+    for (int q = 1; q < p.parts; ++q)
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt) acc[mt] += sums[((wave + q) * kMT + mt) * 64 + lane];
+  }
+#pragma unroll
+  for (int mt = 0; mt < kMT; ++mt) {
+    if (16 * mt + lr >= rows) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t col = n0 + 4 * lq + e;
+      if (col < p.n)
+        store_out(p.y, p.out_bf16, (m0 + 16 * mt + lr) * p.n + col, acc[mt][e] + bias_at(p.bias, p.out_bf16, col));
+    }
+  }
+}
+
+template <bool kBf16X, int kMT>
+hipError_t launch_gemv(GemvArgs a, hipStream_t stream) {
+  int cus = current_device_cus();
+  if (cus <= 0) cus = 256;
+  const int64_t tiles = (a.n + 15) / 16, nblk = (a.k / kGroup + 7) / 8;
+  const int rows = (int)min(a.m, (int64_t)16 * kMT);
+  // row tiles that give every CU one workgroup, and parts of K up to ten waves;
+  // a helper lane carries eight pieces of x, a step as many blocks as that allows
+  constexpr int kPlanes = kBf16X ? 1 : 3;
+  a.tiles = (int)min((tiles + cus - 1) / cus, (int64_t)9);
+  a.parts = 1;
+  while (2 * a.parts * a.tiles <= kGemvComputeMax && 2 * a.parts <= nblk && 2 * a.parts * rows <= 32) a.parts *= 2;
+  const int compute = a.tiles * a.parts;
+  a.blocks = kGemvBlocksMax;
+  while (a.blocks > 1 && (a.parts * a.blocks * rows > 64 || 2 * a.parts * a.blocks * kPlanes * rows * 512 > 64 * 1024))
+    a.blocks /= 2;
+  a.helpers = (a.parts * a.blocks * rows * 32 + 64 * kGemvPieces - 1) / (64 * kGemvPieces);
+  const size_t rest = (size_t)2 * compute * a.blocks * 128 + (size_t)2 * a.parts * a.blocks * kPlanes * rows * 512;
+  const dim3 grid((unsigned)((tiles + a.tiles - 1) / a.tiles), (unsigned)((a.m + 16 * kMT - 1) / (16 * kMT)));
+  const dim3 block(64 * (compute + a.helpers + 1));
+  int depth = 0;
+  size_t lds = 0;
+  for (int d : {8, 6, 4, 3, 2}) {
+    depth = d;
+    lds = rest + (size_t)compute * d * kGemvSlot;
+    if (lds <= 160 * 1024) break;
+  }
+#define FP8BSQ_GEMV(D) hipLaunchKernelGGL((fp4_gemv_kernel<kBf16X, kMT, D>), grid, block, lds, stream, a)
+  switch (depth) {
+    case 8: FP8BSQ_GEMV(8); break;
+    case 6: FP8BSQ_GEMV(6); break;
+    case 4: FP8BSQ_GEMV(4); break;
+    case 3: FP8BSQ_GEMV(3); break;
+    default: FP8BSQ_GEMV(2); break;
+  }
+#undef FP8BSQ_GEMV
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -164,16 +391,11 @@ hipError_t launch_fp4_weight_quant(const void *w, bool w_bf16, int64_t n, int64_
 
 hipError_t launch_fp4_gemv(const void *x, bool x_bf16, const uint8_t *q, const uint8_t *s, const void *bias,
                            void *y, bool y_bf16, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
-  const dim3 grid((unsigned)((n + 15) / 16), (unsigned)((m + 15) / 16)), block(64 * kGemvWaves);
-#define FP8BSQ_GEMV(XB, YB) \
-  hipLaunchKernelGGL((fp4_gemv_kernel<XB, YB>), grid, block, 0, stream, x, q, s, bias, y, m, n, k)
-  if (x_bf16) {
-    if (y_bf16) FP8BSQ_GEMV(true, true); else FP8BSQ_GEMV(true, false);
-  } else {
-    if (y_bf16) FP8BSQ_GEMV(false, true); else FP8BSQ_GEMV(false, false);
-  }
-#undef FP8BSQ_GEMV
-  return hipGetLastError();
+  const GemvArgs a = {x, bias, q, s, y, m, n, k, 1, 1, 1, 1, y_bf16};
+  // fp32 x takes three planes of LDS: 32 rows at a time
+  if (m <= 16) return x_bf16 ? launch_gemv<true, 1>(a, stream) : launch_gemv<false, 1>(a, stream);
+  if (m <= 32 || !x_bf16) return x_bf16 ? launch_gemv<true, 2>(a, stream) : launch_gemv<false, 2>(a, stream);
+  return launch_gemv<true, 4>(a, stream);
 }
 
 }  // namespace fp8bsq
