@@ -76,7 +76,10 @@ __global__ __launch_bounds__(256) void fp4_weight_quant_kernel(const void *__res
 // what the weights meet, a step of `blocks` blocks ahead, through registers: the
 // scales, and x as bf16 planes (each value once per workgroup; fp32 x is split
 // exactly into three bf16, 3 x 8 significand bits, one MFMA each).  One barrier
-// per step hands these on; within a step the waves run freely.  (With fragments
+// per step hands these on; within a step the waves run freely.  Workgroups start
+// at different steps: x's rows often lie a multiple of 4 KB apart, and all
+// workgroups reading the same part of them at once queue at a few L2 channels
+// (16 rows, 18432 x 28672: 137 us in one order for all).  (With fragments
 // loaded straight to registers, 64 bytes of a row at a time, and x read by every
 // wave, 18432 x 7168 and one row took 24 us.)
 // ---------------------------------------------------------------------------
@@ -107,7 +110,8 @@ __device__ __forceinline__ void split3(float (&r)[8], u32x4 (&parts)[3]) {
 
 constexpr int kGemvBlock = 256;        // k per block
 constexpr int kGemvSlot = 16 * 128;    // bytes of codes a wave takes per block
-constexpr int kGemvPieces = 8;         // 8-value pieces of x that a helper lane carries
+// 8-value pieces of x that a helper lane carries
+constexpr int gemv_pieces(bool bf16) { return bf16 ? 8 : 4; }
 constexpr int kGemvBlocksMax = 4;      // blocks per step
 constexpr int kGemvComputeMax = 10, kGemvWavesMax = 16;
 
@@ -116,9 +120,14 @@ struct GemvArgs {
   const uint8_t *q, *s;
   void *y;
   int64_t m, n, k;
-  int tiles, parts, blocks, helpers;
+  int tiles, parts, blocks;   // parts and blocks are powers of two
+  // helper waves: x_groups of x_waves each, and s_groups for the scales; group g
+  // of n brings the steps g, g + n, ..., so a load has n steps' time
+  int x_waves, x_groups, s_groups;
   bool out_bf16;
 };
+
+__device__ __forceinline__ int log2_of(int pow2) { return 31 - __builtin_clz(pow2); }
 
 template <bool kBf16X, int kMT, int kDepth>
 __global__ __launch_bounds__(64 * kGemvWavesMax) void fp4_gemv_kernel(const GemvArgs p) {
@@ -136,71 +145,97 @@ __global__ __launch_bounds__(64 * kGemvWavesMax) void fp4_gemv_kernel(const Gemv
   const int sslot = compute * p.blocks * 128, xslot = p.parts * p.blocks * kPlanes * rows * 512;
   uint8_t *scales = lds + compute * kDepth * kGemvSlot;
   uint8_t *xs = scales + 2 * sslot;
+  // the workgroup's steps, in its own order; prefetches past the last wrap around
+  const int turn = blockIdx.x % steps;
+  auto actual = [&](int step) { return (step + turn) % steps; };
 
   if (wave >= compute) {
-    const int helper = wave - compute;
-    if (helper == p.helpers) {
-      // scales: eight bytes of (compute wave, block, row)
-      constexpr int kEights = (kGemvComputeMax * kGemvBlocksMax * 16 + 63) / 64;
-      const int pieces = compute * p.blocks * 16;
-      uint64_t v[kEights];
-      int64_t src[kEights];   // of step 0
-      int group[kEights];
+    int helper = wave - compute;
+    // a group's turn: step t goes to LDS while step t - 1 is multiplied
+    auto run = [&](int group, int groups, auto load, auto store) {
+      load(group);
+      if (group == 0) {
+        store(0);
+        load(groups);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      workgroup_barrier();
+      int next = group == 0 ? groups : group;   // the step in registers
+      for (int step = 0; step < steps; ++step) {
+        if (step + 1 == next) {
+          store(next);   // into the buffer of step - 1
+          next += groups;
+          load(next);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        workgroup_barrier();
+      }
+    };
+    if (helper < p.s_groups) {
+      // scales: 16 bytes, two blocks' (one's and eight unused, with one block a
+      // step), of (compute wave, row)
+      constexpr int kPieces = (kGemvComputeMax * kGemvBlocksMax / 2 * 16 + 63) / 64;
+      const int per_row = max(p.blocks / 2, 1), pieces = compute * per_row * 16;
+      u32x4 v[kPieces];
+      int64_t src[kPieces];   // of actual step 0
+      int group[kPieces];
 #pragma unroll
-      for (int i = 0; i < kEights; ++i) {
-        const int idx = i * 64 + lane, w = idx / (p.blocks * 16), b = (idx >> 4) - w * p.blocks;
-        const int64_t row = min(((int64_t)blockIdx.x * p.tiles + w / p.parts) * 16 + (idx & 15), p.n - 1);
-        group[i] = 8 * (w % p.parts * per + b);
+      for (int i = 0; i < kPieces; ++i) {
+        const int idx = i * 64 + lane, wb = idx >> 4, w = wb >> log2_of(per_row), b = 2 * (wb & (per_row - 1));
+        const int64_t row = min(((int64_t)blockIdx.x * p.tiles + (w >> log2_of(p.parts))) * 16 + (idx & 15), p.n - 1);
+        group[i] = 8 * ((w & (p.parts - 1)) * per + b);
         src[i] = row * ng + group[i];
       }
       auto load = [&](int step) {
+        const int ahead = 8 * actual(step) * p.blocks;
 #pragma unroll
-        for (int i = 0; i < kEights; ++i) {
-          const int ahead = 8 * step * p.blocks, left = ng - group[i] - ahead;
-          v[i] = 0;
+        for (int i = 0; i < kPieces; ++i) {
+          const int left = ng - group[i] - ahead;
+          v[i] = u32x4{0, 0, 0, 0};
           if (i * 64 + lane >= pieces || left <= 0) continue;
-          if (src[i] + ahead + 8 <= p.n * ng)   // past the row's end lies the next row's, unused
-            __builtin_memcpy(&v[i], p.s + src[i] + ahead, 8);
+          if (src[i] + ahead + 16 <= p.n * ng)   // past the row's end lies the next row's, unused
+            __builtin_memcpy(&v[i], p.s + src[i] + ahead, 16);
           else
-            for (int c = 0; c < 8 && c < left; ++c) v[i] |= (uint64_t)p.s[src[i] + ahead + c] << (8 * c);
+            for (int c = 0; c < 16 && c < left; ++c) v[i][c >> 2] |= (uint32_t)p.s[src[i] + ahead + c] << (8 * (c & 3));
         }
       };
       auto store = [&](int step) {
 #pragma unroll
-        for (int i = 0; i < kEights; ++i)
-          if (i * 64 + lane < pieces) *(uint64_t *)(scales + (step & 1) * sslot + (i * 64 + lane) * 8) = v[i];
+        for (int i = 0; i < kPieces; ++i) {
+          const int idx = i * 64 + lane;
+          if (idx >= pieces) continue;
+          const int wb = idx >> 4, w = wb >> log2_of(per_row), b = 2 * (wb & (per_row - 1));
+          uint8_t *dst = scales + (step & 1) * sslot + ((w * p.blocks + b) * 16 + (idx & 15)) * 8;
+          *(u32x2 *)dst = u32x2{v[i][0], v[i][1]};
+          if (p.blocks > 1) *(u32x2 *)(dst + 128) = u32x2{v[i][2], v[i][3]};
+        }
       };
-      load(0);
-      store(0);
-      load(1);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      workgroup_barrier();
-      for (int step = 0; step < steps; ++step) {
-        store(step + 1);   // into the buffer of step - 1
-        load(step + 2);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        workgroup_barrier();
-      }
+      run(helper, p.s_groups, load, store);
     } else {
       // x: eight values of (part, block, row)
-      const int pieces = p.parts * p.blocks * rows * 32, stride = p.helpers * 64;
-      u32x4 v[kGemvPieces][kBf16X ? 1 : 2];
-      int64_t base[kGemvPieces];   // the row's first value
-      int k0[kGemvPieces], dst[kGemvPieces];
+      constexpr int kPieces = gemv_pieces(kBf16X);
+      helper -= p.s_groups;
+      int group = 0;
+      for (; helper >= p.x_waves; helper -= p.x_waves) ++group;
+      const int pieces = p.parts * p.blocks * rows * 32, stride = p.x_waves * 64, inverse = (65535 + rows) / rows;
+      u32x4 v[kPieces][kBf16X ? 1 : 2];
+      int64_t base[kPieces];   // the row's first value
+      int k0[kPieces], dst[kPieces];
 #pragma unroll
-      for (int i = 0; i < kGemvPieces; ++i) {
-        const int idx = i * stride + helper * 64 + lane, pb = idx / (rows * 32), row = (idx >> 5) - pb * rows;
-        const int part = pb / p.blocks, b = pb - part * p.blocks;
+      for (int i = 0; i < kPieces; ++i) {
+        // (part, block) by the rows' inverse, exact for the at most 512 pieces / 32
+        const int idx = i * stride + helper * 64 + lane, pb = ((idx >> 5) * inverse) >> 16, row = (idx >> 5) - pb * rows;
+        const int part = pb >> log2_of(p.blocks), b = pb & (p.blocks - 1);
         base[i] = (m0 + row) * p.k;
         k0[i] = (part * per + b) * kGemvBlock + 8 * (idx & 31);
         dst[i] = (pb * kPlanes * rows + row) * 512 + (((idx & 31) ^ (row & 15)) << 4);
       }
       auto load = [&](int step) {
 #pragma unroll
-        for (int i = 0; i < kGemvPieces; ++i) {
+        for (int i = 0; i < kPieces; ++i) {
           if (i * stride + helper * 64 + lane >= pieces) continue;
           // past the end any x will do: the codes it meets are zero
-          const int64_t at = base[i] + min(k0[i] + step * p.blocks * kGemvBlock, (int)p.k - 8);
+          const int64_t at = base[i] + min(k0[i] + actual(step) * p.blocks * kGemvBlock, (int)p.k - 8);
           if constexpr (kBf16X) {
             v[i][0] = *(const u32x4 *)((const uint16_t *)p.x + at);
           } else {
@@ -212,7 +247,7 @@ __global__ __launch_bounds__(64 * kGemvWavesMax) void fp4_gemv_kernel(const Gemv
       auto store = [&](int step) {
         uint8_t *slot = xs + (step & 1) * xslot;
 #pragma unroll
-        for (int i = 0; i < kGemvPieces; ++i) {
+        for (int i = 0; i < kPieces; ++i) {
           if (i * stride + helper * 64 + lane >= pieces) continue;
           if constexpr (kBf16X) {
             *(u32x4 *)(slot + dst[i]) = v[i][0];
@@ -230,17 +265,7 @@ __global__ __launch_bounds__(64 * kGemvWavesMax) void fp4_gemv_kernel(const Gemv
           }
         }
       };
-      load(0);
-      store(0);
-      load(1);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      workgroup_barrier();
-      for (int step = 0; step < steps; ++step) {
-        store(step + 1);   // into the slot of step - 1
-        load(step + 2);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        workgroup_barrier();
-      }
+      run(group, p.x_groups, load, store);
     }
     if (p.parts > 1) {   // the compute waves' sums
       workgroup_barrier();
@@ -249,7 +274,7 @@ __global__ __launch_bounds__(64 * kGemvWavesMax) void fp4_gemv_kernel(const Gemv
     return;
   }
 
-  const int tile = wave / p.parts, part = wave - tile * p.parts;
+  const int tile = wave >> log2_of(p.parts), part = wave & (p.parts - 1);
   const int64_t n0 = ((int64_t)blockIdx.x * p.tiles + tile) * 16;
   const int64_t nc = min(n0, p.n - 1);   // rows past the last re-read it
   const int lr = lane & 15, lq = lane >> 4, dr = lane >> 3, ds = lane & 7;
@@ -260,8 +285,12 @@ __global__ __launch_bounds__(64 * kGemvWavesMax) void fp4_gemv_kernel(const Gemv
   const int chunk[2] = {ds ^ swz(dr), ds ^ swz(8 + dr)};
   const uint8_t *ring = lds + wave * kDepth * kGemvSlot;
   const uint32_t lds_ring = lds_addr(ring);
+  const int blocks_log2 = log2_of(p.blocks);
+  auto block_of = [&](int j) {   // the j-th block of the workgroup's order, in the part
+    return (actual(j >> blocks_log2) << blocks_log2) + (j & (p.blocks - 1));
+  };
   auto issue = [&](int j) {   // groups past a row's end re-read its last one; so do blocks past the end
-    const int blk = max(min(blk0 + j, blk1 - 1), 0);
+    const int blk = max(min(blk0 + block_of(j), blk1 - 1), 0);
     const uint32_t slot = lds_ring + (uint32_t)(j % kDepth) * kGemvSlot;
 #pragma unroll
     for (int i = 0; i < 2; ++i) lds_dma16(base, row_off[i] + (uint32_t)min(8 * blk + chunk[i], ng - 1) * 16, slot + i * 1024);
@@ -275,9 +304,8 @@ __global__ __launch_bounds__(64 * kGemvWavesMax) void fp4_gemv_kernel(const Gemv
     for (int mt = 0; mt < kMT; ++mt) sum[h][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
   workgroup_barrier();
   for (int step = 0; step < steps; ++step) {
-    const int end = min((step + 1) * p.blocks, blk1 - blk0);
-    for (int j = step * p.blocks; j < end; ++j) {
-      const int b = j - step * p.blocks;
+    for (int b = 0; b < p.blocks; ++b) {
+      const int j = step * p.blocks + b, blk = blk0 + block_of(j);
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (kDepth - 1)) : "memory");   // block j landed
       const uint8_t *slot = ring + j % kDepth * kGemvSlot + lr * 128;
       u32x4 codes[2];
@@ -286,12 +314,13 @@ __global__ __launch_bounds__(64 * kGemvWavesMax) void fp4_gemv_kernel(const Gemv
       const uint32_t sc = *(const uint16_t *)(scales + (step & 1) * sslot + ((wave * p.blocks + b) * 16 + lr) * 8 + 2 * lq);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read: the slot may be refilled
       issue(j + kDepth);
+      if (blk >= blk1) continue;
       const uint8_t *xb = xs + (step & 1) * xslot + (part * p.blocks + b) * kPlanes * rows * 512;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const bool live = 8 * (blk0 + j) + 2 * lq + h < ng;
+          const bool live = 8 * blk + 2 * lq + h < ng;
           const float scale = pow2_scale(live ? (sc >> (8 * h)) & 0xFFu : 127u);
           const bf16x8 w = fp4_to_bf16(live ? codes[h][t] : 0u, scale);
 #pragma unroll
@@ -343,8 +372,8 @@ hipError_t launch_gemv(GemvArgs a, hipStream_t stream) {
   if (cus <= 0) cus = 256;
   const int64_t tiles = (a.n + 15) / 16, nblk = (a.k / kGroup + 7) / 8;
   const int rows = (int)min(a.m, (int64_t)16 * kMT);
-  // row tiles that give every CU one workgroup, and parts of K up to ten waves;
-  // a helper lane carries eight pieces of x, a step as many blocks as that allows
+  // row tiles that give every CU one workgroup, parts of K up to ten waves, and as
+  // many blocks a step as LDS and the helpers' registers hold of x
   constexpr int kPlanes = kBf16X ? 1 : 3;
   a.tiles = (int)min((tiles + cus - 1) / cus, (int64_t)9);
   a.parts = 1;
@@ -353,10 +382,14 @@ hipError_t launch_gemv(GemvArgs a, hipStream_t stream) {
   a.blocks = kGemvBlocksMax;
   while (a.blocks > 1 && (a.parts * a.blocks * rows > 64 || 2 * a.parts * a.blocks * kPlanes * rows * 512 > 64 * 1024))
     a.blocks /= 2;
-  a.helpers = (a.parts * a.blocks * rows * 32 + 64 * kGemvPieces - 1) / (64 * kGemvPieces);
+  constexpr int kLane = 64 * gemv_pieces(kBf16X);
+  a.x_waves = (a.parts * a.blocks * rows * 32 + kLane - 1) / kLane;
+  const int spare = kGemvWavesMax - compute;
+  a.x_groups = max(1, min(4, (spare - 1) / a.x_waves));
+  a.s_groups = max(1, min(4, spare - a.x_groups * a.x_waves));
   const size_t rest = (size_t)2 * compute * a.blocks * 128 + (size_t)2 * a.parts * a.blocks * kPlanes * rows * 512;
   const dim3 grid((unsigned)((tiles + a.tiles - 1) / a.tiles), (unsigned)((a.m + 16 * kMT - 1) / (16 * kMT)));
-  const dim3 block(64 * (compute + a.helpers + 1));
+  const dim3 block(64 * (compute + a.s_groups + a.x_groups * a.x_waves));
   int depth = 0;
   size_t lds = 0;
   for (int d : {8, 6, 4, 3, 2}) {
@@ -391,7 +424,16 @@ hipError_t launch_fp4_weight_quant(const void *w, bool w_bf16, int64_t n, int64_
 
 hipError_t launch_fp4_gemv(const void *x, bool x_bf16, const uint8_t *q, const uint8_t *s, const void *bias,
                            void *y, bool y_bf16, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
-  const GemvArgs a = {x, bias, q, s, y, m, n, k, 1, 1, 1, 1, y_bf16};
+  GemvArgs a = {};
+  a.x = x;
+  a.bias = bias;
+  a.q = q;
+  a.s = s;
+  a.y = y;
+  a.m = m;
+  a.n = n;
+  a.k = k;
+  a.out_bf16 = y_bf16;
   // fp32 x takes three planes of LDS: 32 rows at a time
   if (m <= 16) return x_bf16 ? launch_gemv<true, 1>(a, stream) : launch_gemv<false, 1>(a, stream);
   if (m <= 32 || !x_bf16) return x_bf16 ? launch_gemv<true, 2>(a, stream) : launch_gemv<false, 2>(a, stream);
