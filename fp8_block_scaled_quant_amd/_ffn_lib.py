@@ -51,4 +51,19 @@ def lib() -> ctypes.CDLL:
     return _LIB or load_library()
 
 
-check = _lib.check
+_EXT = None
+
+
+def ext():
+    """The native Python binding over the library (``_ffn_ext.so``); raises if absent."""
+    global _EXT
+    if _EXT is None:
+        load_library()
+        _lib.lib()
+        try:
+            from . import _ffn_ext
+        except ImportError as e:
+            raise ImportError("fp8_block_scaled_quant_amd/_ffn_ext.so is missing or does not load: build the HIP "
+                              "library first (python -m fp8_block_scaled_quant_amd.build)") from e
+        _EXT = _ffn_ext
+    return _EXT

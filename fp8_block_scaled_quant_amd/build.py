@@ -1,6 +1,7 @@
 """Compile the HIP sources into the in-tree shared libraries ``libfp8bsq.so`` (the
 quantizers and the block-scaled GEMM) and ``libfp8bsq_ffn.so`` (the feed-forward
-operators, which call the first).
+operators, which call the first), and the latter's Python binding ``_ffn_ext.so``
+(host code over torch's headers).
 
 gfx950 only.  Packed-FP32 instruction selection is switched off for every HIP
 source, floating-point contraction is off unless a kernel asks for a fused
@@ -25,6 +26,8 @@ FFN_LIB_PATH = os.path.join(PKG_DIR, FFN_LIB_NAME)
 
 SOURCES = ["abi.cpp", "act_quant.hip", "weight_dequant.hip", "weight_quant.hip", "block_gemm.hip"]
 FFN_SOURCES = ["ffn_abi.cpp", "gated_ffn.hip", "gated_ffn_backward.hip", "fp4.hip", "grad_clip.hip"]
+BINDING_SOURCE = "ffn_binding.cpp"
+BINDING_PATH = os.path.join(PKG_DIR, "_ffn_ext.so")
 
 HIP_FLAGS = [
     "--offload-arch=gfx950",
@@ -50,6 +53,8 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
     objdir = os.path.join(PKG_DIR, "_build")
     os.makedirs(objdir, exist_ok=True)
     cc = hipcc()
+    binding = (BINDING_SOURCE, subprocess.Popen(_binding_command(objdir, verbose), stdout=subprocess.PIPE,
+                                                stderr=subprocess.STDOUT))
     procs = []
     objs = {src: os.path.join(objdir, src + ".o") for src in SOURCES + FFN_SOURCES}
     # the slowest source first, so that the others compile beside it
@@ -67,7 +72,29 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
     _link(cc, [objs[s] for s in SOURCES], [], LIB_PATH, verbose)
     # found beside it at run time
     _link(cc, [objs[s] for s in FFN_SOURCES], ["-L", PKG_DIR, "-lfp8bsq", "-Wl,-rpath,$ORIGIN"], FFN_LIB_PATH, verbose)
+    _drain([binding])
+    from torch.utils import cpp_extension
+    dirs = [arg for d in cpp_extension.library_paths() for arg in ("-L", d, "-Wl,-rpath," + d)]
+    _link(cc, [os.path.join(objdir, BINDING_SOURCE + ".o")],
+          ["-L", PKG_DIR, "-lfp8bsq_ffn", "-Wl,-rpath,$ORIGIN", *dirs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_hip"], BINDING_PATH, verbose)
     return LIB_PATH
+
+
+def _binding_command(objdir, verbose):
+    """The binding's compile command: host code only, torch's own compile-time definitions."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__",
+           "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"],
+           *[arg for d in cpp_extension.include_paths("cuda") for arg in ("-isystem", d)],
+           "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", os.path.join(objdir, BINDING_SOURCE + ".o")]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    return cmd
 
 
 def _link(cc, objs, libs, path, verbose):

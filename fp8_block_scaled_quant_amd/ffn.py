@@ -8,16 +8,19 @@ kernels; tensors on the CPU raise.
 
 import torch
 
-from . import _DTYPE, _SCALE_FMT, _codes, _ffn_lib, _require_gpu, _stream_handle, weight_quant
+from . import _DTYPE, _SCALE_FMT, _ffn_lib, weight_quant
 
 
-def _weight(name, w, w_s, f, k):
-    if w.dim() != 2 or tuple(w.shape) != (f, k):
-        raise ValueError(f"{name} must be [{f}, {k}], got {tuple(w.shape)}")
-    if w_s.dtype != torch.float32:
-        raise TypeError("scales must be float32")
-    if tuple(w_s.shape) != (-(-f // 128), k // 128):
-        raise ValueError(f"{name}'s scales must be [ceil(F/128), K/128]")
+def _format(scale_fmt):
+    if scale_fmt not in _SCALE_FMT:
+        raise ValueError(f"unknown scale_fmt {scale_fmt!r}")
+    return _SCALE_FMT[scale_fmt]
+
+
+def _out(dtype):
+    if dtype not in _DTYPE:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    return _DTYPE[dtype]
 
 
 def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_gate_s: torch.Tensor, w_up: torch.Tensor,
@@ -29,35 +32,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_gate_s: torch.Tensor, w_u
     ``out_dtype``, or with ``save`` the tuple ``(h, g, u)``: what
     ``gated_ffn_backward`` takes.
     """
-    w_gate, w_up = _codes(w_gate), _codes(w_up)
-    _require_gpu(x, w_gate, w_gate_s, w_up, w_up_s)
-    if x.dtype not in _DTYPE:
-        raise TypeError("gated_ffn takes bf16 or fp32 activations")
-    if scale_fmt not in _SCALE_FMT:
-        raise ValueError(f"unknown scale_fmt {scale_fmt!r}")
-    if out_dtype not in _DTYPE:
-        raise TypeError("out_dtype must be float32 or bfloat16")
-    k = x.shape[-1]
-    if k <= 0 or k % 128 != 0:
-        raise ValueError("K must be a positive multiple of 128")
-    f = w_gate.shape[0]
-    _weight("w_gate", w_gate, w_gate_s, f, k)
-    _weight("w_up", w_up, w_up_s, f, k)
-    m = x.numel() // k
-    shape = x.shape[:-1] + (f,)
-    h = torch.empty(shape, dtype=out_dtype, device=x.device)
-    g, u = (torch.empty_like(h), torch.empty_like(h)) if save else (None, None)
-    if m and f:
-        lib = _ffn_lib.lib()
-        nbytes = lib.fp8_gated_ffn_workspace(m, f, k)
-        # torch's allocator keeps the workspace from being reused until the
-        # work queued on this stream has passed it
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        _ffn_lib.check(lib.fp8_gated_ffn(
-            x.data_ptr(), _DTYPE[x.dtype], _SCALE_FMT[scale_fmt], w_gate.data_ptr(), w_gate_s.data_ptr(),
-            w_up.data_ptr(), w_up_s.data_ptr(), h.data_ptr(), g.data_ptr() if save else None,
-            u.data_ptr() if save else None, _DTYPE[out_dtype], m, f, k, ws.data_ptr(), nbytes, _stream_handle(x)))
-    return (h, g, u) if save else h
+    return _ffn_lib.ext().gated_ffn(x, w_gate, w_gate_s, w_up, w_up_s, _format(scale_fmt), _out(out_dtype), save)
 
 
 def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor, u: torch.Tensor, w_gate: torch.Tensor,
@@ -72,32 +47,8 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor, u: to
     (and, for the weights, ``x``) are rounded with one power-of-two scale per 128
     values along each contraction.  F must be a multiple of 128.
     """
-    w_gate, w_up = _codes(w_gate), _codes(w_up)
-    _require_gpu(dh, x, g, u, w_gate, w_gate_s, w_up, w_up_s)
-    if dh.dtype not in _DTYPE or any(t.dtype != dh.dtype for t in (x, g, u)):
-        raise TypeError("dh, x, g and u must all be bf16 or all fp32")
-    if out_dtype not in _DTYPE:
-        raise TypeError("out_dtype must be float32 or bfloat16")
-    f, k = dh.shape[-1], x.shape[-1]
-    if f <= 0 or f % 128 != 0 or k <= 0 or k % 128 != 0:
-        raise ValueError("F and K must be positive multiples of 128")
-    if g.shape != dh.shape or u.shape != dh.shape or x.shape[:-1] != dh.shape[:-1]:
-        raise ValueError("g and u must have dh's shape, and x its leading dimensions")
-    _weight("w_gate", w_gate, w_gate_s, f, k)
-    _weight("w_up", w_up, w_up_s, f, k)
-    m = x.numel() // k
-    dx = torch.empty(x.shape, dtype=out_dtype, device=x.device) if input_grad else None
-    dwg, dwu = (torch.empty((f, k), dtype=out_dtype, device=x.device) for _ in range(2)) if weight_grad else (None, None)
-    if weight_grad or (input_grad and m):
-        lib = _ffn_lib.lib()
-        nbytes = lib.fp8_gated_ffn_backward_workspace(m, f, k)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        _ffn_lib.check(lib.fp8_gated_ffn_backward(
-            dh.data_ptr(), x.data_ptr(), g.data_ptr(), u.data_ptr(), _DTYPE[dh.dtype], w_gate.data_ptr(),
-            w_gate_s.data_ptr(), w_up.data_ptr(), w_up_s.data_ptr(), dx.data_ptr() if input_grad else None,
-            dwg.data_ptr() if weight_grad else None, dwu.data_ptr() if weight_grad else None, _DTYPE[out_dtype],
-            m, f, k, ws.data_ptr(), nbytes, _stream_handle(x)))
-    return dx, dwg, dwu
+    return _ffn_lib.ext().gated_ffn_backward(dh, x, g, u, w_gate, w_gate_s, w_up, w_up_s, _out(out_dtype), input_grad,
+                                             weight_grad)
 
 
 class _GatedFFNFunction(torch.autograd.Function):
