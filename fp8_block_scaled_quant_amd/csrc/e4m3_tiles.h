@@ -40,7 +40,6 @@ struct TileArgs {
   int nkb;                  // blocks of the contraction
   int half;                 // kInput: blocks of the first weight
   int tiles_a, tiles_b, parts;
-  bool vec;                 // kGated: four outputs of a row make one aligned store
 };
 
 // Swizzle of a tile read transposed, rows of 128 or 256 bytes: the 16-byte chunk
@@ -79,18 +78,27 @@ __device__ __forceinline__ float load_uniform(const float *p, int64_t i) {
 
 __device__ __forceinline__ int exponent_of(float pow2) { return (int)((__float_as_uint(pow2) >> 23) & 0xFFu); }
 
-// silu(g) * u; the exponential overflows to infinity for g below -88, where
-// the sigmoid is 0 to fp32's precision.
-__device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// silu(g) * u; the reciprocal instruction is within one ulp; the exponential
+// overflows to infinity for g below -88, where the sigmoid is 0 to fp32's
+// precision.
+__device__ __forceinline__ float gated(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
 
-// Four consecutive outputs of a row, or those of them inside it.
-template <bool kBf16Out>
-__device__ __forceinline__ void store4(void *p, int64_t idx, f32x4 v, bool vec, int left) {
-  if (vec && left >= 4) {
-    if (kBf16Out)
-      *(u32x2 *)((uint16_t *)p + idx) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    else
-      *(f32x4 *)((float *)p + idx) = v;
+// Row `row` of a tile with `left` rows of the matrix from its first (at least
+// one): rows past the matrix re-read its last.
+__device__ __forceinline__ uint32_t tile_row(int row, int64_t left) {
+  return (uint32_t)min(row, (int)min(left, (int64_t)kBlock * 2) - 1);
+}
+
+// Four consecutive outputs of a row: one store (kVec; the row has all four), or
+// one each for the `left` that are inside the row.
+template <bool kBf16Out, bool kVec>
+__device__ __forceinline__ void store4(void *p, int64_t idx, f32x4 v, int left) {
+  if (kVec && kBf16Out) {
+    *(u32x2 *)((uint16_t *)p + idx) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  } else if (kVec) {
+    *(f32x4 *)((float *)p + idx) = v;
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -99,15 +107,15 @@ __device__ __forceinline__ void store4(void *p, int64_t idx, f32x4 v, bool vec, 
 }
 
 // h, and with them g and u, of four consecutive features.
-template <bool kBf16Out>
-__device__ __forceinline__ void store_gated(const TileArgs &p, int64_t idx, f32x4 g, f32x4 u, int left) {
+template <bool kBf16Out, bool kVec>
+__device__ __forceinline__ void store_gated(void *h, void *g_out, void *u_out, int64_t idx, f32x4 g, f32x4 u, int left) {
   f32x4 v;
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = gated(g[e], u[e]);
-  store4<kBf16Out>(p.out0, idx, v, p.vec, left);
-  if (p.out1) {
-    store4<kBf16Out>(p.out1, idx, g, p.vec, left);
-    store4<kBf16Out>(p.out2, idx, u, p.vec, left);
+  store4<kBf16Out, kVec>(h, idx, v, left);
+  if (g_out) {
+    store4<kBf16Out, kVec>(g_out, idx, g, left);
+    store4<kBf16Out, kVec>(u_out, idx, u, left);
   }
 }
 
@@ -151,7 +159,7 @@ __device__ __forceinline__ void big_tile_coords(int it, int tiles_a, int tiles_b
   tb = idx / ga;
 }
 
-template <TileMode kMode, bool kMx, bool kBf16Out>
+template <TileMode kMode, bool kMx, bool kBf16Out, bool kVec>
 __global__ __launch_bounds__(kBigThreads) void e4m3_big_kernel(const TileArgs p) {
   static_assert(kMode == TileMode::kGated || kMx, "gradient scales are powers of two");
   constexpr bool kGatedMode = kMode == TileMode::kGated, kInputMode = kMode == TileMode::kInput;
@@ -180,18 +188,18 @@ __global__ __launch_bounds__(kBigThreads) void e4m3_big_kernel(const TileArgs p)
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
       const int row = 8 * (8 * dw + g) + dr;
-      a_off[g] = (uint32_t)((min(a0 + row, p.rows_a - 1) - a0) * p.lda + ((ds ^ swz(row)) << 4));
+      a_off[g] = tile_row(row, p.rows_a - a0) * (uint32_t)p.lda + ((ds ^ swz(row)) << 4);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (kInputMode) {   // 128 features x 256 of the weights' columns
         const int row = 4 * (4 * wave + i) + (lane >> 4);
-        const int64_t col = b0 + (((lane & 15) ^ swz_tr<256>(row)) << 4);
-        b_off[i] = (uint32_t)(row * p.ldb + min(col, p.rows_b - 16) - b0);
+        const int col = ((lane & 15) ^ swz_tr<256>(row)) << 4;
+        b_off[i] = row * (uint32_t)p.ldb + tile_row(col, p.rows_b - 15 - b0);
       } else {
         const int row = 8 * (4 * wave + i) + dr;   // kGated: half row / 128, projection (row / 64) % 2
-        const int64_t r = b0 + (kGatedMode ? (row >> 7) * 64 + (row & 63) : row);
-        b_off[i] = (uint32_t)((min(r, p.rows_b - 1) - b0) * p.ldb + ((ds ^ swz(row)) << 4));
+        const int r = kGatedMode ? (row >> 7) * 64 + (row & 63) : row;
+        b_off[i] = tile_row(r, p.rows_b - b0) * (uint32_t)p.ldb + ((ds ^ swz(row)) << 4);
       }
     }
     as_base = p.a_s + a0 + 64 * dw;
@@ -360,14 +368,15 @@ __global__ __launch_bounds__(kBigThreads) void e4m3_big_kernel(const TileArgs p)
         for (int j = 0; j < 4; ++j) {
           const int64_t col = b0 + 64 * wb + 16 * j + 4 * fq;
           if (col < p.rows_b)
-            store_gated<kBf16Out>(p, row * p.rows_b + col, acc[i][j], acc[i][j + 4], (int)min((int64_t)4, p.rows_b - col));
+            store_gated<kBf16Out, kVec>(p.out0, p.out1, p.out2, row * p.rows_b + col, acc[i][j], acc[i][j + 4],
+                                        (int)min((int64_t)4, p.rows_b - col));
         }
       } else if (b0 + 128 * wb < p.rows_b) {   // whole blocks of 128 columns
         const int64_t f = p.rows_a / 2;
         const bool second = kWeightMode && row >= f;
         const int64_t at = (second ? row - f : row) * p.rows_b + b0 + 128 * wb + 4 * fq;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) store4<kBf16Out>(second ? p.out1 : p.out0, at + 16 * j, acc[i][j], true, 4);
+        for (int j = 0; j < 8; ++j) store4<kBf16Out, true>(second ? p.out1 : p.out0, at + 16 * j, acc[i][j], 4);
       }
     }
   }
@@ -406,7 +415,7 @@ __device__ __forceinline__ float *mid_partial(const TileArgs &p, int tile, int p
   return p.partials + ((size_t)tile * p.parts + part) * (kMidTile * kMidTile) + wave * 4096 + i * 1024 + lane * 4;
 }
 
-template <TileMode kMode, bool kBf16Out>
+template <TileMode kMode, bool kBf16Out, bool kVec>
 __device__ __forceinline__ void mid_finish(const TileArgs &p, int ta, int tb, int wave, int i, int lane,
                                            const f32x4 (&acc)[4]) {
   const int fr = lane & 15, fq = lane >> 4, wb = wave & 1;
@@ -417,20 +426,21 @@ __device__ __forceinline__ void mid_finish(const TileArgs &p, int ta, int tb, in
     for (int j = 0; j < 2; ++j) {
       const int64_t col = (int64_t)tb * (kMidTile / 2) + 32 * wb + 16 * j + 4 * fq;
       if (col < p.rows_b)
-        store_gated<kBf16Out>(p, row * p.rows_b + col, acc[j], acc[j + 2], (int)min((int64_t)4, p.rows_b - col));
+        store_gated<kBf16Out, kVec>(p.out0, p.out1, p.out2, row * p.rows_b + col, acc[j], acc[j + 2],
+                                    (int)min((int64_t)4, p.rows_b - col));
     }
   } else {
     const int64_t f = p.rows_a / 2;
     const bool second = kMode == TileMode::kWeight && row >= f;
     const int64_t at = (second ? row - f : row) * p.rows_b + (int64_t)tb * kMidTile + 64 * wb + 4 * fq;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) store4<kBf16Out>(second ? p.out1 : p.out0, at + 16 * j, acc[j], true, 4);
+    for (int j = 0; j < 4; ++j) store4<kBf16Out, true>(second ? p.out1 : p.out0, at + 16 * j, acc[j], 4);
   }
 }
 
 // kMx: the columns' scales are powers of two and go into the MFMA.
 // Workgroup `block` of the `total` that the product takes.
-template <TileMode kMode, bool kMx, bool kBf16Out>
+template <TileMode kMode, bool kMx, bool kBf16Out, bool kVec>
 __device__ __forceinline__ void mid_tile(const TileArgs &p, int block, int total, MidSlot *ring) {
   static_assert(kMode == TileMode::kGated || kMx, "gradient scales are powers of two");
   constexpr bool kGatedMode = kMode == TileMode::kGated, kInputMode = kMode == TileMode::kInput;
@@ -459,11 +469,11 @@ __device__ __forceinline__ void mid_tile(const TileArgs &p, int block, int total
     for (int i = 0; i < 16; ++i) {
       const int row = 8 * i + dr;
       if (!rows_mover)
-        off[i] = (uint32_t)((min(a0 + row, p.rows_a - 1) - a0) * p.lda + ((ds ^ swz(row)) << 4));
+        off[i] = tile_row(row, p.rows_a - a0) * (uint32_t)p.lda + ((ds ^ swz(row)) << 4);
       else if (kGatedMode)   // half row / 64, projection (row / 32) % 2
-        off[i] = (uint32_t)((min(b0 + (row >> 6) * 32 + (row & 31), p.rows_b - 1) - b0) * p.ldb + ((ds ^ swz(row)) << 4));
+        off[i] = tile_row((row >> 6) * 32 + (row & 31), p.rows_b - b0) * (uint32_t)p.ldb + ((ds ^ swz(row)) << 4);
       else
-        off[i] = (uint32_t)(row * p.ldb + ((ds ^ (kInputMode ? swz_tr<kBlock>(row) : swz(row))) << 4));
+        off[i] = row * (uint32_t)p.ldb + ((ds ^ (kInputMode ? swz_tr<kBlock>(row) : swz(row))) << 4);
     }
     const uint32_t lds_ring = lds_addr(&ring[0]) + (rows_mover ? kMidTile * kBlock : 0);
     const uint32_t s_off = (uint32_t)lane * 4;
@@ -618,20 +628,20 @@ __device__ __forceinline__ void mid_tile(const TileArgs &p, int block, int total
 #pragma unroll
       for (int j = 0; j < 4; ++j) *(f32x4 *)(out + j * 256) = acc[i][j];
     } else {
-      mid_finish<kMode, kBf16Out>(p, ta, tb, wave, i, lane, acc[i]);
+      mid_finish<kMode, kBf16Out, kVec>(p, ta, tb, wave, i, lane, acc[i]);
     }
   }
 }
 
-template <TileMode kMode, bool kMx, bool kBf16Out>
+template <TileMode kMode, bool kMx, bool kBf16Out, bool kVec>
 __global__ __launch_bounds__(kMidThreads) void e4m3_mid_kernel(const TileArgs p) {
   __shared__ __attribute__((aligned(1024))) MidSlot ring[kMidSlots];
-  mid_tile<kMode, kMx, kBf16Out>(p, blockIdx.x, gridDim.x, ring);
+  mid_tile<kMode, kMx, kBf16Out, kVec>(p, blockIdx.x, gridDim.x, ring);
 }
 
 // Adds a tile's partials in part order: block 4 tile + i the column tiles i of
 // the tile's four waves (256 threads).
-template <TileMode kMode, bool kBf16Out>
+template <TileMode kMode, bool kBf16Out, bool kVec>
 __device__ __forceinline__ void mid_reduce(const TileArgs &p, int block) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tile = block >> 2, i = block & 3;
@@ -642,12 +652,12 @@ __device__ __forceinline__ void mid_reduce(const TileArgs &p, int block) {
   for (int q = 1; q < p.parts; ++q)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] += *(const f32x4 *)(mid_partial(p, tile, q, wave, i, lane) + j * 256);
-  mid_finish<kMode, kBf16Out>(p, tile % p.tiles_a, tile / p.tiles_a, wave, i, lane, acc);
+  mid_finish<kMode, kBf16Out, kVec>(p, tile % p.tiles_a, tile / p.tiles_a, wave, i, lane, acc);
 }
 
-template <TileMode kMode, bool kBf16Out>
+template <TileMode kMode, bool kBf16Out, bool kVec>
 __global__ __launch_bounds__(256) void e4m3_reduce_kernel(const TileArgs p) {
-  mid_reduce<kMode, kBf16Out>(p, blockIdx.x);
+  mid_reduce<kMode, kBf16Out, kVec>(p, blockIdx.x);
 }
 
 // How a product of `nkb` blocks is launched: 256 x 256 tiles, or 128 x 128
@@ -698,33 +708,23 @@ inline TilePlan tile_plan(int64_t cols, int64_t rows, int row_tile, int nkb, int
   return mid_us < big_us ? mid : big;
 }
 
-// Launch by plan.  a.partials: the plan's bytes, if any.
-template <TileMode kMode, bool kMx>
-inline hipError_t launch_tiles(const TilePlan &plan, TileArgs a, bool out_bf16, int cus, hipStream_t stream) {
+// Launch by plan.  a.partials: the plan's bytes, if any.  kVec: every four
+// outputs of a row make one aligned store.
+template <TileMode kMode, bool kMx, bool kBf16Out, bool kVec>
+inline hipError_t launch_tiles(const TilePlan &plan, TileArgs a, int cus, hipStream_t stream) {
   if (cus <= 0) cus = 256;
   plan.fill(a);
   const int64_t tiles = (int64_t)plan.tiles_a * plan.tiles_b;
   if (plan.big) {
-    const dim3 grid((unsigned)(tiles < cus ? tiles : cus)), block(kBigThreads);
-    if (out_bf16)
-      hipLaunchKernelGGL((e4m3_big_kernel<kMode, kMx, true>), grid, block, 0, stream, a);
-    else
-      hipLaunchKernelGGL((e4m3_big_kernel<kMode, kMx, false>), grid, block, 0, stream, a);
-  } else {
-    const dim3 grid((unsigned)(tiles * plan.parts)), block(kMidThreads);
-    if (out_bf16)
-      hipLaunchKernelGGL((e4m3_mid_kernel<kMode, kMx, true>), grid, block, 0, stream, a);
-    else
-      hipLaunchKernelGGL((e4m3_mid_kernel<kMode, kMx, false>), grid, block, 0, stream, a);
-    if (plan.parts > 1) {
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-      if (out_bf16)
-        hipLaunchKernelGGL((e4m3_reduce_kernel<kMode, true>), dim3((unsigned)(tiles * 4)), dim3(256), 0, stream, a);
-      else
-        hipLaunchKernelGGL((e4m3_reduce_kernel<kMode, false>), dim3((unsigned)(tiles * 4)), dim3(256), 0, stream, a);
-    }
+    const dim3 grid((unsigned)(tiles < cus ? tiles : cus));
+    hipLaunchKernelGGL((e4m3_big_kernel<kMode, kMx, kBf16Out, kVec>), grid, dim3(kBigThreads), 0, stream, a);
+    return hipGetLastError();
   }
+  const dim3 grid((unsigned)(tiles * plan.parts));
+  hipLaunchKernelGGL((e4m3_mid_kernel<kMode, kMx, kBf16Out, kVec>), grid, dim3(kMidThreads), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || plan.parts == 1) return e;
+  hipLaunchKernelGGL((e4m3_reduce_kernel<kMode, kBf16Out, kVec>), dim3((unsigned)(tiles * 4)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -79,7 +79,7 @@ int fp8_gated_ffn_backward(const void *dh, const void *x, const void *g, const v
   if (!dh || !g || !u || !workspace || (dx && (!w_gate || !w_gate_s || !w_up || !w_up_s)) || (dw_gate && !x))
     return FP8BSQ_EINVAL;
   if (!aligned(dh, 16) || !aligned(g, 16) || !aligned(u, 16) || !aligned(x, 16) || !aligned(w_gate, 16) ||
-      !aligned(w_up, 16) || !aligned(w_gate_s, 4) || !aligned(w_up_s, 4) || !aligned(dx, 4) ||
+      !aligned(w_up, 16) || !aligned(w_gate_s, 4) || !aligned(w_up_s, 4) || !aligned(dx, 16) ||
       !aligned(dw_gate, 16) || !aligned(dw_up, 16) || !aligned(workspace, 256))
     return FP8BSQ_EALIGN;
   if (!ffn_sizes_ok(m, f, k)) return FP8BSQ_ERANGE;

@@ -210,16 +210,15 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void gated_decode_kernel(const D
   for (int e = 0; e < 4; ++e) upper[e] = __shfl_xor(acc[e], 32);
   const int64_t col = f0 + 4 * fq;
   if (fq >= 2 || !live || col >= p.f) return;
-  TileArgs o = {};
-  o.out0 = p.h;
-  o.out1 = p.g;
-  o.out2 = p.u;
-  o.vec = p.vec;
   const int left = (int)min((int64_t)4, p.f - col);
-  if (p.out_bf16)
-    store_gated<true>(o, fr * p.f + col, acc, upper, left);
-  else
-    store_gated<false>(o, fr * p.f + col, acc, upper, left);
+  const int64_t at = fr * p.f + col;
+  if (p.out_bf16) {
+    if (p.vec) store_gated<true, true>(p.h, p.g, p.u, at, acc, upper, 4);
+    else store_gated<true, false>(p.h, p.g, p.u, at, acc, upper, left);
+  } else {
+    if (p.vec) store_gated<false, true>(p.h, p.g, p.u, at, acc, upper, 4);
+    else store_gated<false, false>(p.h, p.g, p.u, at, acc, upper, left);
+  }
 }
 
 // How the decode kernel is launched; depth 0: it does not take these sizes.
@@ -315,7 +314,6 @@ hipError_t launch_gated_ffn(const void *x, bool x_bf16, bool ue8m0, const uint8_
   p.lda = p.ldb = k;
   p.a_stride = rows_padded(m);
   p.nkb = (int)(k / kBlock);
-  p.vec = vec;
 
   const dim3 grid((unsigned)((m + kQuantRows - 1) / kQuantRows), (unsigned)((p.nkb + kQuantKb - 1) / kQuantKb));
 #define FP8BSQ_QUANT(BF, UE)                                                                                   \
@@ -330,8 +328,13 @@ hipError_t launch_gated_ffn(const void *x, bool x_bf16, bool ue8m0, const uint8_
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int cus = current_device_cus();
-  return ue8m0 ? launch_tiles<TileMode::kGated, true>(plan, p, out_bf16, cus, stream)
-               : launch_tiles<TileMode::kGated, false>(plan, p, out_bf16, cus, stream);
+#define FP8BSQ_GATED(MX, BF, VEC) launch_tiles<TileMode::kGated, MX, BF, VEC>(plan, p, cus, stream)
+#define FP8BSQ_GATED_OUT(MX)                                                    \
+  (out_bf16 ? (vec ? FP8BSQ_GATED(MX, true, true) : FP8BSQ_GATED(MX, true, false)) \
+            : (vec ? FP8BSQ_GATED(MX, false, true) : FP8BSQ_GATED(MX, false, false)))
+  return ue8m0 ? FP8BSQ_GATED_OUT(true) : FP8BSQ_GATED_OUT(false);
+#undef FP8BSQ_GATED_OUT
+#undef FP8BSQ_GATED
 }
 
 }  // namespace fp8bsq

@@ -73,8 +73,12 @@ __device__ __forceinline__ void store_tokens(const float (&v)[kLaneRows][8], Tok
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     top[c] = max(max(abs_bits(v[0][c]), abs_bits(v[1][c])), max(abs_bits(v[2][c]), abs_bits(v[3][c])));
-    top[c] = max(top[c], (uint32_t)__shfl_xor((int)top[c], 16));
-    top[c] = max(top[c], (uint32_t)__shfl_xor((int)top[c], 32));
+    // against the lane 16, then 32 away: the swap of a value with itself leaves
+    // one of the pair's two in every lane of either result
+    const auto far16 = __builtin_amdgcn_permlane16_swap(top[c], top[c], false, false);
+    top[c] = max(far16[0], far16[1]);
+    const auto far32 = __builtin_amdgcn_permlane32_swap(top[c], top[c], false, false);
+    top[c] = max(far32[0], far32[1]);
   }
   if (grp == 0) {
     *(u32x4 *)&sm.colmax[wave][8 * sub] = u32x4{top[0], top[1], top[2], top[3]};
@@ -140,21 +144,22 @@ struct QuantArgs {
   int64_t cs_stride;
   uint8_t *xq;   // [k][mpad], with cq
   float *xs;     // [mpad / 128][k]
-  int grad_tiles, split;
+  int grad_tiles;
 };
 
-// Everything that the products read, in one launch: workgroups below
-// grad_tiles * split quantize a tile of dg and du, the others a tile of x.  With
-// fewer tiles than CUs the tile's four results (dg or du, along the features or
-// the tokens) go to a workgroup each (split = 4), which all form the gradient
-// anew: 333 x 1024 took 15 us in one piece, its arithmetic on 24 CUs.
-template <bool kBf16>
+// Everything that the products read, in one launch: the first workgroups
+// quantize a tile of dg and du each, the others a tile of x.  With fewer tiles
+// than CUs (kSplit) the tile's four results (dg or du, along the features or the
+// tokens) go to a workgroup each: 333 x 1024 took 15 us in one piece, its
+// arithmetic on 24 CUs.
+template <bool kBf16, bool kSplit>
 __global__ __launch_bounds__(kQuantThreads) void ffn_quant_kernel(const QuantArgs p) {
   __shared__ TokenTile sm;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lane_row = kLaneRows * (4 * wave + (lane >> 4)), lane_col = 8 * (lane & 15);
-  if ((int)blockIdx.x >= p.grad_tiles * p.split) {
-    const int tile = blockIdx.x - p.grad_tiles * p.split, across = (int)(p.k / kBlock);
+  const int grads = p.grad_tiles * (kSplit ? 4 : 1);
+  if ((int)blockIdx.x >= grads) {
+    const int tile = blockIdx.x - grads, across = (int)(p.k / kBlock);
     const int64_t m0 = (int64_t)(tile / across) * kBlock, k0 = (int64_t)(tile % across) * kBlock;
     float v[kLaneRows][8];
 #pragma unroll
@@ -165,40 +170,63 @@ __global__ __launch_bounds__(kQuantThreads) void ffn_quant_kernel(const QuantArg
     store_tokens(v, sm, p.xq, p.xs + m0 / kBlock * p.k, k0, m0, p.mpad);
     return;
   }
-  const int tile = blockIdx.x / p.split, piece = blockIdx.x % p.split, across = (int)(p.f / kBlock);
+  const int tile = kSplit ? blockIdx.x >> 2 : blockIdx.x, across = (int)(p.f / kBlock);
   const int64_t m0 = (int64_t)(tile / across) * kBlock, f0 = (int64_t)(tile % across) * kBlock;
-  const bool all = p.split == 1;
-  const bool rows = p.rq && (all || piece < 2), tokens = p.cq && (all || piece >= 2);
-  if (!rows && !tokens) return;
   const int64_t row0 = m0 + lane_row;
-  float dg[kLaneRows][8], du[kLaneRows][8];
+  // one of the two gradients from dh, g, u
+  auto grad = [](bool gate, float h, float g, float u) {
+    // the reciprocal instruction is within one ulp; exp overflows to infinity
+    // for g below -88, where the sigmoid is 0 to fp32's precision
+    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+    return gate ? h * u * (s * __builtin_fmaf(g, 1.0f - s, 1.0f)) : h * (g * s);
+  };
+  auto along_rows = [&](const float (&v)[kLaneRows][8], bool gate) {
+    store_rows(v, p.rq + (gate ? 0 : p.f) + f0 + lane_col, 2 * p.f,
+               p.rs + (f0 + (gate ? 0 : p.f)) / kBlock * p.rs_stride, row0, p.m);
+  };
+  auto along_tokens = [&](const float (&v)[kLaneRows][8], bool gate) {
+    store_tokens(v, sm, p.cq, p.cs + m0 / kBlock * p.cs_stride, (gate ? 0 : p.f) + f0, m0, p.mpad);
+  };
+  float hv[kLaneRows][8], gv[kLaneRows][8], uv[kLaneRows][8];
+  if (kSplit) {
+    const bool gate = (blockIdx.x & 1) == 0, rows = (blockIdx.x & 2) == 0;
+    if (rows ? !p.rq : !p.cq) return;
+#pragma unroll
+    for (int r = 0; r < kLaneRows; ++r) {
+      const bool live = row0 + r < p.m;
+      const int64_t idx = (row0 + r) * p.f + f0 + lane_col;
+      load8<kBf16>(p.dh, idx, live, hv[r]);
+      load8<kBf16>(p.g, idx, live, gv[r]);
+      load8<kBf16>(p.u, idx, live && gate, uv[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < kLaneRows; ++r)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) hv[r][c] = grad(gate, hv[r][c], gv[r][c], uv[r][c]);
+    if (rows) along_rows(hv, gate); else along_tokens(hv, gate);
+    return;
+  }
 #pragma unroll
   for (int r = 0; r < kLaneRows; ++r) {
     const bool live = row0 + r < p.m;
     const int64_t idx = (row0 + r) * p.f + f0 + lane_col;
-    float hv[8], gv[8], uv[8];
-    load8<kBf16>(p.dh, idx, live, hv);
-    load8<kBf16>(p.g, idx, live, gv);
-    load8<kBf16>(p.u, idx, live, uv);
+    load8<kBf16>(p.dh, idx, live, hv[r]);
+    load8<kBf16>(p.g, idx, live, gv[r]);
+    load8<kBf16>(p.u, idx, live, uv[r]);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      // the reciprocal instruction is within one ulp; exp overflows to infinity
-      // for g below -88, where the sigmoid is 0 to fp32's precision
-      const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-gv[c]));
-      du[r][c] = hv[c] * (gv[c] * s);
-      dg[r][c] = hv[c] * uv[c] * (s * __builtin_fmaf(gv[c], 1.0f - s, 1.0f));
+      const float h = hv[r][c], g = gv[r][c];
+      hv[r][c] = grad(true, h, g, uv[r][c]);
+      gv[r][c] = grad(false, h, g, uv[r][c]);
     }
   }
-  const bool gate = all || (piece & 1) == 0, up = all || (piece & 1) == 1;
-  if (rows) {
-    float *s = p.rs + f0 / kBlock * p.rs_stride;
-    if (gate) store_rows(dg, p.rq + f0 + lane_col, 2 * p.f, s, row0, p.m);
-    if (up) store_rows(du, p.rq + p.f + f0 + lane_col, 2 * p.f, s + p.f / kBlock * p.rs_stride, row0, p.m);
+  if (p.rq) {
+    along_rows(hv, true);
+    along_rows(gv, false);
   }
-  if (tokens) {
-    float *s = p.cs + m0 / kBlock * p.cs_stride;
-    if (gate) store_tokens(dg, sm, p.cq, s, f0, m0, p.mpad);
-    if (up) store_tokens(du, sm, p.cq, s, p.f + f0, m0, p.mpad);
+  if (p.cq) {
+    along_tokens(hv, true);
+    along_tokens(gv, false);
   }
 }
 
@@ -208,17 +236,17 @@ template <bool kBf16Out>
 __global__ __launch_bounds__(kMidThreads) void mid_pair_kernel(const TileArgs in, const TileArgs wt, int first) {
   __shared__ __attribute__((aligned(1024))) MidSlot ring[kMidSlots];
   if ((int)blockIdx.x < first)
-    mid_tile<TileMode::kInput, true, kBf16Out>(in, blockIdx.x, first, ring);
+    mid_tile<TileMode::kInput, true, kBf16Out, true>(in, blockIdx.x, first, ring);
   else
-    mid_tile<TileMode::kWeight, true, kBf16Out>(wt, blockIdx.x - first, gridDim.x - first, ring);
+    mid_tile<TileMode::kWeight, true, kBf16Out, true>(wt, blockIdx.x - first, gridDim.x - first, ring);
 }
 
 template <bool kBf16Out>
 __global__ __launch_bounds__(256) void reduce_pair_kernel(const TileArgs in, const TileArgs wt, int first) {
   if ((int)blockIdx.x < first)
-    mid_reduce<TileMode::kInput, kBf16Out>(in, blockIdx.x);
+    mid_reduce<TileMode::kInput, kBf16Out, true>(in, blockIdx.x);
   else
-    mid_reduce<TileMode::kWeight, kBf16Out>(wt, blockIdx.x - first);
+    mid_reduce<TileMode::kWeight, kBf16Out, true>(wt, blockIdx.x - first);
 }
 
 hipError_t launch_mid_pair(const TilePlan &in, TileArgs pi, const TilePlan &wt, TileArgs pw, bool out_bf16,
@@ -296,12 +324,16 @@ hipError_t launch_gated_ffn_backward(const void *dh, const void *x, const void *
     q.xs = (float *)(base + ws.xs);
     const int64_t grad_tiles = (f / kBlock) * (mpad / kBlock), x_tiles = dwg ? (k / kBlock) * (mpad / kBlock) : 0;
     q.grad_tiles = (int)grad_tiles;
-    q.split = grad_tiles < (cus > 0 ? cus : 256) ? 4 : 1;
-    const dim3 grid((unsigned)(grad_tiles * q.split + x_tiles));
-    if (in_bf16)
-      hipLaunchKernelGGL(ffn_quant_kernel<true>, grid, dim3(kQuantThreads), 0, stream, q);
-    else
-      hipLaunchKernelGGL(ffn_quant_kernel<false>, grid, dim3(kQuantThreads), 0, stream, q);
+    const bool split = grad_tiles < (cus > 0 ? cus : 256);
+    const dim3 grid((unsigned)(grad_tiles * (split ? 4 : 1) + x_tiles));
+#define FP8BSQ_FFN_QUANT(BF, SPLIT) \
+  hipLaunchKernelGGL((ffn_quant_kernel<BF, SPLIT>), grid, dim3(kQuantThreads), 0, stream, q)
+    if (in_bf16) {
+      if (split) FP8BSQ_FFN_QUANT(true, true); else FP8BSQ_FFN_QUANT(true, false);
+    } else {
+      if (split) FP8BSQ_FFN_QUANT(false, true); else FP8BSQ_FFN_QUANT(false, false);
+    }
+#undef FP8BSQ_FFN_QUANT
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -337,10 +369,13 @@ hipError_t launch_gated_ffn_backward(const void *dh, const void *x, const void *
   const bool want_dx = dx && m > 0;
   if (want_dx && dwg && !in.big && !wt.big) return launch_mid_pair(in, pi, wt, pw, out_bf16, stream);
   if (want_dx) {
-    const hipError_t e = launch_tiles<TileMode::kInput, true>(in, pi, out_bf16, cus, stream);
+    const hipError_t e = out_bf16 ? launch_tiles<TileMode::kInput, true, true, true>(in, pi, cus, stream)
+                                  : launch_tiles<TileMode::kInput, true, false, true>(in, pi, cus, stream);
     if (e != hipSuccess) return e;
   }
-  return dwg ? launch_tiles<TileMode::kWeight, true>(wt, pw, out_bf16, cus, stream) : hipSuccess;
+  if (!dwg) return hipSuccess;
+  return out_bf16 ? launch_tiles<TileMode::kWeight, true, true, true>(wt, pw, cus, stream)
+                  : launch_tiles<TileMode::kWeight, true, false, true>(wt, pw, cus, stream);
 }
 
 }  // namespace fp8bsq

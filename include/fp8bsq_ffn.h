@@ -74,8 +74,7 @@ FP8BSQ_API size_t fp8_gated_ffn_workspace(int64_t m, int64_t f, int64_t k);
  *                then be NULL).
  *   dw_gate, dw_up  [f, k] out, or both NULL: not computed (x is not read and
  *                may then be NULL).
- *                Outputs have dtype out_dtype; dx is 4-byte, dw_.. are 16-byte
- *                aligned.
+ *                Outputs have dtype out_dtype and are 16-byte aligned.
  *   m, f, k      m, f, k >= 0, f and k multiples of 128 (else FP8BSQ_ESHAPE).
  *                f = 0 or k = 0 is FP8BSQ_EINVAL.  m = 0: dw_gate and dw_up are
  *                set to zero, and nothing else is read or written.
