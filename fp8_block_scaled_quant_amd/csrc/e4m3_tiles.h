@@ -674,10 +674,13 @@ struct TilePlan {
   }
 };
 
-// The cheaper of the two by their time per CU: a block of a 256 x 256 tile takes
-// kBigBlockUs, one of a 128 x 128 tile kMidBlockUs, and a split tile's partial
-// sums kSplitUs more.
-constexpr double kBigBlockUs = 1.8, kMidBlockUs = 0.7, kSplitUs = 5.0;
+// The cheaper of the two by their time on a CU: a round of tiles takes so much
+// per block of 128 and so much besides, and a split product's second kernel so
+// much more.  Measured (gated_ffn, us, 256 against 128 tiles): 2048 x 2048 x 2048
+// 34 and 37, 4096 x 1024 x 1024 23 and 28, 512 x 4096 x 4096 49 and 28,
+// 700 x 1000 x 896 17 and 12; 211 x 2300 x 7168 76, 38 and 25 in three parts,
+// 300 x 640 x 4096 49, 26 and 21 in eight.
+constexpr double kBigBlockUs = 1.65, kBigRoundUs = 4.0, kMidBlockUs = 0.65, kMidRoundUs = 5.0, kSplitUs = 5.0;
 
 // cols: rows of the columns operand; rows: rows of the rows operand in tiles of
 // row_tile (of a 256 x 256 tile; half that in a 128 x 128 one).
@@ -687,20 +690,21 @@ inline TilePlan tile_plan(int64_t cols, int64_t rows, int row_tile, int nkb, int
   TilePlan big, mid;
   big.tiles_a = (int)ceil_div(cols, kBigTile);
   big.tiles_b = (int)ceil_div(rows, row_tile);
-  const double big_us = (double)ceil_div((int64_t)big.tiles_a * big.tiles_b, cus) * nkb * kBigBlockUs;
+  const double big_us = (double)ceil_div((int64_t)big.tiles_a * big.tiles_b, cus) * (nkb * kBigBlockUs + kBigRoundUs);
   mid.big = false;
   mid.tiles_a = (int)ceil_div(cols, kMidTile);
   mid.tiles_b = (int)ceil_div(rows, row_tile / 2);
   const int64_t tiles = (int64_t)mid.tiles_a * mid.tiles_b;
   if (tiles == 0) return big;   // nothing to launch
-  double mid_us = (double)ceil_div(tiles, cus) * nkb * kMidBlockUs;
+  double mid_us = (double)ceil_div(tiles, cus) * (nkb * kMidBlockUs + kMidRoundUs);
   // fill the CUs once; four blocks a part at least, or the ring never runs full
   const int64_t most = min(min((int64_t)cus / tiles, (int64_t)nkb / 4), (int64_t)kMidPartsMax);
   if (most >= 2) {
     const int per = (int)ceil_div(nkb, most);
     const int parts = (int)ceil_div(nkb, per);   // parts that get any, as the kernel divides them
-    if (parts >= 2 && per * kMidBlockUs + kSplitUs < mid_us) {
-      mid_us = per * kMidBlockUs + kSplitUs;
+    const double split_us = per * kMidBlockUs + kMidRoundUs + kSplitUs;
+    if (parts >= 2 && split_us < mid_us) {
+      mid_us = split_us;
       mid.parts = parts;
       mid.partial_bytes = (size_t)tiles * parts * kMidTile * kMidTile * sizeof(float);
     }
