@@ -79,9 +79,11 @@ __global__ __launch_bounds__(256) void fp4_weight_quant_kernel(const void *__res
 // per step hands these on; within a step the waves run freely.  Workgroups start
 // at different steps: x's rows often lie a multiple of 4 KB apart, and all
 // workgroups reading the same part of them at once queue at a few L2 channels
-// (16 rows, 18432 x 28672: 137 us in one order for all).  (With fragments
-// loaded straight to registers, 64 bytes of a row at a time, and x read by every
-// wave, 18432 x 7168 and one row took 24 us.)
+// (16 rows, 18432 x 28672: 137 us in one order for all).
+//
+// Measured, 18432 x 7168 (70.2 MB of codes and scales): one row 19 us, 3.7 TB/s;
+// 16 rows 23 us.  Fragments loaded straight to registers, 64 bytes of a row at a
+// time, with x read by every wave, took 24 us for one row.
 // ---------------------------------------------------------------------------
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -120,6 +122,7 @@ struct GemvArgs {
   const uint8_t *q, *s;
   void *y;
   int64_t m, n, k;
+  int rows;                   // of x per workgroup
   int tiles, parts, blocks;   // parts and blocks are powers of two
   // helper waves: x_groups of x_waves each, and s_groups for the scales; group g
   // of n brings the steps g, g + n, ..., so a load has n steps' time
@@ -138,8 +141,8 @@ __global__ __launch_bounds__(64 * kGemvWavesMax) void fp4_gemv_kernel(const Gemv
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int compute = p.tiles * p.parts;
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * kMT);
-  const int rows = (int)min((int64_t)16 * kMT, p.m - m0);
+  const int64_t m0 = (int64_t)blockIdx.y * p.rows;
+  const int rows = (int)min((int64_t)p.rows, p.m - m0);
   const int ng = (int)(p.k / kGroup), nblk = (ng + 7) / 8, per = (nblk + p.parts - 1) / p.parts;
   const int steps = (per + p.blocks - 1) / p.blocks;
   const int sslot = compute * p.blocks * 128, xslot = p.parts * p.blocks * kPlanes * rows * 512;
@@ -371,7 +374,7 @@ hipError_t launch_gemv(GemvArgs a, hipStream_t stream) {
   int cus = current_device_cus();
   if (cus <= 0) cus = 256;
   const int64_t tiles = (a.n + 15) / 16, nblk = (a.k / kGroup + 7) / 8;
-  const int rows = (int)min(a.m, (int64_t)16 * kMT);
+  const int rows = a.rows;
   // row tiles that give every CU one workgroup, parts of K up to ten waves, and as
   // many blocks a step as LDS and the helpers' registers hold of x
   constexpr int kPlanes = kBf16X ? 1 : 3;
@@ -388,7 +391,7 @@ hipError_t launch_gemv(GemvArgs a, hipStream_t stream) {
   a.x_groups = max(1, min(4, (spare - 1) / a.x_waves));
   a.s_groups = max(1, min(4, spare - a.x_groups * a.x_waves));
   const size_t rest = (size_t)2 * compute * a.blocks * 128 + (size_t)2 * a.parts * a.blocks * kPlanes * rows * 512;
-  const dim3 grid((unsigned)((tiles + a.tiles - 1) / a.tiles), (unsigned)((a.m + 16 * kMT - 1) / (16 * kMT)));
+  const dim3 grid((unsigned)((tiles + a.tiles - 1) / a.tiles), (unsigned)((a.m + rows - 1) / rows));
   const dim3 block(64 * (compute + a.s_groups + a.x_groups * a.x_waves));
   int depth = 0;
   size_t lds = 0;
@@ -434,9 +437,20 @@ hipError_t launch_fp4_gemv(const void *x, bool x_bf16, const uint8_t *q, const u
   a.n = n;
   a.k = k;
   a.out_bf16 = y_bf16;
-  // fp32 x takes three planes of LDS: 32 rows at a time
-  if (m <= 16) return x_bf16 ? launch_gemv<true, 1>(a, stream) : launch_gemv<false, 1>(a, stream);
-  if (m <= 32 || !x_bf16) return x_bf16 ? launch_gemv<true, 2>(a, stream) : launch_gemv<false, 2>(a, stream);
+  int cus = current_device_cus();
+  if (cus <= 0) cus = 256;
+  // Rows of x a workgroup: fp32 x takes three planes of LDS, and 32 rows of them
+  // leave room for two waves' rings (64 rows, 18432 x 7168: 233 us against 147 by
+  // 16; 64 bf16 rows: 59).  Where row tiles leave CUs idle the rows go to several
+  // workgroups, which read the weights from the caches (32 fp32 rows,
+  // 1000 x 2048: 9 us against 27 with 16 rows or more each).
+  const int64_t tiles = (n + 15) / 16, most = x_bf16 ? 64 : 16;
+  int64_t rows = m < most ? m : most;
+  while (rows > 4 && tiles * ((m + (rows + 1) / 2 - 1) / ((rows + 1) / 2)) <= cus) rows = (rows + 1) / 2;
+  a.rows = (int)rows;
+  if (!x_bf16) return launch_gemv<false, 1>(a, stream);
+  if (rows <= 16) return launch_gemv<true, 1>(a, stream);
+  if (rows <= 32) return launch_gemv<true, 2>(a, stream);
   return launch_gemv<true, 4>(a, stream);
 }
 
