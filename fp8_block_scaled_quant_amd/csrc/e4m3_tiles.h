@@ -680,7 +680,7 @@ struct TilePlan {
 // 34 and 37, 4096 x 1024 x 1024 23 and 28, 512 x 4096 x 4096 49 and 28,
 // 700 x 1000 x 896 17 and 12; 211 x 2300 x 7168 76, 38 and 25 in three parts,
 // 300 x 640 x 4096 49, 26 and 21 in eight.
-constexpr double kBigBlockUs = 1.65, kBigRoundUs = 4.0, kMidBlockUs = 0.65, kMidRoundUs = 5.0, kSplitUs = 5.0;
+constexpr double kBigBlockUs = 1.65, kBigRoundUs = 8.0, kMidBlockUs = 0.65, kMidRoundUs = 7.5, kSplitUs = 5.0;
 
 // cols: rows of the columns operand; rows: rows of the rows operand in tiles of
 // row_tile (of a 256 x 256 tile; half that in a 128 x 128 one).
