@@ -15,7 +15,8 @@ constexpr int kGroup = 32;
 // E2M1(w / s), round to nearest even.  w / s is exact (a power of two), so the
 // conversion instruction's rounding is the only one.  Groups of the whole
 // weight form one sequence (k is a multiple of 32); four lanes own a group,
-// eight weights each.
+// eight weights each.  Bound by memory: 18432 x 7168 bf16 (334 MB) 56 us,
+// 6 TB/s.
 // ---------------------------------------------------------------------------
 template <bool kBf16>
 __global__ __launch_bounds__(256) void fp4_weight_quant_kernel(const void *__restrict__ w, int64_t ngroups,

@@ -47,6 +47,7 @@ __device__ __forceinline__ void load_block(const void *x, int64_t block, int sub
 // kernels' transfers read them.  Sixteen lanes own a 1 x 128 block, 8 values
 // each; a workgroup takes 16 rows and up to four consecutive K blocks of them,
 // so a row is read in 1 KB runs (bf16) and 16 rows' scales are written together.
+// Bound by memory: 8192 x 7168 bf16 36 us, 4.9 TB/s; small ones by the launch.
 constexpr int kQuantRows = 16, kQuantKb = 4;
 
 template <bool kBf16, bool kUe8m0>
@@ -91,9 +92,11 @@ __global__ __launch_bounds__(256) void ffn_act_quant_kernel(const void *__restri
 // themselves would wait for their own older weight transfers first.  They go in
 // K order in up to kPhases pieces, a barrier after each, so that the K loop
 // starts on the first piece.
+//
+// Measured, one row, 18432 x 7168 (264 MB of weights): 48 us, 5.5 TB/s, above a
+// 1 GiB copy's 5.1; the first, simple kernel took 110 us.
 // ---------------------------------------------------------------------------
 constexpr int kDecodeRows = 16, kDecodeWaves = 16, kDecodeFeatures = 8, kPhases = 4;
-constexpr int kDecodeComputeMax = 12;
 
 struct DecodeArgs {
   const void *x;

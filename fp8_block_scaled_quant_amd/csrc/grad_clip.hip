@@ -10,6 +10,12 @@
 // ran first.  Tensor addresses travel in the kernel arguments, kTableTensors a
 // launch: nothing is uploaded and nothing kept between calls.  The tensors of a
 // table form one sequence of chunks that the workgroups walk.
+//
+// Bound by memory: the factor needs every gradient before the first is scaled,
+// so they are read twice and written once.  396 M elements of bf16 (2.4 GB in
+// all) take 435 us, 5.5 TB/s; the second pass backwards, for what the last cache
+// still holds, took 440.  240 small tensors take 12 us, two launches'
+// latency.
 #include "ffn_launch.h"
 #include "device_common.h"
 
