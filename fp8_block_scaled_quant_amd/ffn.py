@@ -95,7 +95,10 @@ class GatedFFN(torch.nn.Module):
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
-        return _GatedFFNFunction.apply(x.to(self.w_gate.dtype), self.w_gate, self.w_up, self.scale_fmt)
+        x = x.to(self.w_gate.dtype)
+        if not torch.is_grad_enabled():   # g and u need not be stored
+            return gated_ffn(x.contiguous(), *weight_quant(self.w_gate), *weight_quant(self.w_up), self.scale_fmt, x.dtype)
+        return _GatedFFNFunction.apply(x, self.w_gate, self.w_up, self.scale_fmt)
 
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, hidden_features={self.hidden_features}, "

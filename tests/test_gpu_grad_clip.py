@@ -39,10 +39,11 @@ def _check(grads, outs, norm, max_norm, eps=1e-6):
 
 
 BF, F32 = torch.bfloat16, torch.float32
-# one value; less than a vector; the ends of a chunk of 16384; tables of 96
-# tensors exactly, one more, and three of them
+# one value; less than a vector; the ends of a chunk of 16384; a table of 256
+# tensors exactly, one more, and three tables
 CASES = [([1], [F32]), ([3], [BF]), ([7, 0, 9], [BF, F32, F32]), ([16384, 16383, 16385], [BF, F32, BF]),
          ([40001, 5], [F32, BF]), ([10] * 96, [BF] * 96), ([11] * 97, [F32, BF] * 49), ([300 + i for i in range(200)], [BF, F32] * 100),
+         ([13] * 256, [F32, BF] * 128), ([20 + i % 7 for i in range(257)], [BF] * 256 + [F32]), ([i % 40 for i in range(600)], [BF, F32] * 300),
          ([3_000_001, 17], [BF, F32])]
 
 
