@@ -63,8 +63,11 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 }
 
 struct TokenTile {
-  uint8_t codes[128 * 128];               // [column][token], 16-byte pieces swizzled by the column
-  uint32_t colmax[kQuantWaves][128];
+  // [column][token]: 16-byte pieces swizzled by the column's 8, and columns 64
+  // on in swapped pairs, so that a wave's stores, 16 columns apart by 8, touch
+  // all banks once
+  uint8_t codes[128 * 128];
+  uint32_t colmax[kQuantWaves][2][64];    // columns 8 i .. + 3, and 8 i + 4 .. + 7, of lane i
 };
 
 // Quantize a tile's values v [4 rows][8 columns] along the rows (tokens) and
@@ -85,15 +88,15 @@ __device__ __forceinline__ void store_tokens(const float (&v)[kLaneRows][8], Tok
     top[c] = max(far32[0], far32[1]);
   }
   if (grp == 0) {
-    *(u32x4 *)&sm.colmax[wave][8 * sub] = u32x4{top[0], top[1], top[2], top[3]};
-    *(u32x4 *)&sm.colmax[wave][8 * sub + 4] = u32x4{top[4], top[5], top[6], top[7]};
+    *(u32x4 *)&sm.colmax[wave][0][4 * sub] = u32x4{top[0], top[1], top[2], top[3]};
+    *(u32x4 *)&sm.colmax[wave][1][4 * sub] = u32x4{top[4], top[5], top[6], top[7]};
   }
   __syncthreads();
-  u32x4 lo = *(const u32x4 *)&sm.colmax[0][8 * sub], hi = *(const u32x4 *)&sm.colmax[0][8 * sub + 4];
+  u32x4 lo = *(const u32x4 *)&sm.colmax[0][0][4 * sub], hi = *(const u32x4 *)&sm.colmax[0][1][4 * sub];
 #pragma unroll
   for (int w = 1; w < kQuantWaves; ++w) {
-    lo = __builtin_elementwise_max(lo, *(const u32x4 *)&sm.colmax[w][8 * sub]);
-    hi = __builtin_elementwise_max(hi, *(const u32x4 *)&sm.colmax[w][8 * sub + 4]);
+    lo = __builtin_elementwise_max(lo, *(const u32x4 *)&sm.colmax[w][0][4 * sub]);
+    hi = __builtin_elementwise_max(hi, *(const u32x4 *)&sm.colmax[w][1][4 * sub]);
   }
   const int piece = wave;   // 16 tokens
 #pragma unroll
@@ -101,7 +104,7 @@ __device__ __forceinline__ void store_tokens(const float (&v)[kLaneRows][8], Tok
     const int col = 8 * sub + c;
     const uint32_t e = e4m3_scale_byte(c < 4 ? lo[c & 3] : hi[c & 3]);
     const float inv = pow2_inverse(e);
-    *(uint32_t *)&sm.codes[col * 128 + ((piece ^ (sub & 7)) << 4) + 4 * grp] =
+    *(uint32_t *)&sm.codes[(col ^ (sub >> 3)) * 128 + ((piece ^ (sub & 7)) << 4) + 4 * grp] =
         codes4(v[0][c] * inv, v[1][c] * inv, v[2][c] * inv, v[3][c] * inv);
     if (wave == 0 && grp == 0) scales[row0 + col] = pow2_scale(e);
   }
@@ -110,7 +113,7 @@ __device__ __forceinline__ void store_tokens(const float (&v)[kLaneRows][8], Tok
   for (int i = 0; i < 128 * 8 / kQuantThreads; ++i) {
     const int idx = i * kQuantThreads + t, col = idx >> 3, j = idx & 7;
     *(u32x4 *)(out + (row0 + col) * mpad + m0 + 16 * j) =
-        *(const u32x4 *)&sm.codes[col * 128 + ((j ^ ((col >> 3) & 7)) << 4)];
+        *(const u32x4 *)&sm.codes[(col ^ (col >> 6)) * 128 + ((j ^ ((col >> 3) & 7)) << 4)];
   }
   __syncthreads();   // the tile may be reused
 }
