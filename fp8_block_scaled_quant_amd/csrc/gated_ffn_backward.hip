@@ -29,9 +29,10 @@ namespace {
 // and a column's four rows pack into one 4-byte piece of the transposed tile,
 // which goes through LDS to whole-line stores.
 //
-// Measured, 4096 x 18432 and x 4096 x 7168: 843 MB in 217-235 us, 3.7 TB/s; two
-// workgroups a CU, whose barriers leave loads and arithmetic (some 60
-// instructions an element) half overlapped.
+// Measured, 4096 x 18432 and x 4096 x 7168: 843 MB in 199 us, 4.2 TB/s; the
+// arithmetic, some 50 instructions an element, is 60% of that and overlaps the
+// loads of the CU's other workgroup only.  Stores that met half the banks made it
+// 225 us, every thread reducing the waves' column maxima for itself 212.
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 512, kQuantWaves = kQuantThreads / 64, kLaneRows = 4;
 
@@ -67,7 +68,8 @@ struct TokenTile {
   // on in swapped pairs, so that a wave's stores, 16 columns apart by 8, touch
   // all banks once
   uint8_t codes[128 * 128];
-  uint32_t colmax[kQuantWaves][2][64];    // columns 8 i .. + 3, and 8 i + 4 .. + 7, of lane i
+  uint32_t colmax[128][kQuantWaves + 1];   // padded: a lane's eight columns, 8 apart, in different banks
+  float inverse[128];
 };
 
 // Quantize a tile's values v [4 rows][8 columns] along the rows (tokens) and
@@ -88,25 +90,27 @@ __device__ __forceinline__ void store_tokens(const float (&v)[kLaneRows][8], Tok
     top[c] = max(far32[0], far32[1]);
   }
   if (grp == 0) {
-    *(u32x4 *)&sm.colmax[wave][0][4 * sub] = u32x4{top[0], top[1], top[2], top[3]};
-    *(u32x4 *)&sm.colmax[wave][1][4 * sub] = u32x4{top[4], top[5], top[6], top[7]};
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sm.colmax[8 * sub + c][wave] = top[c];
   }
   __syncthreads();
-  u32x4 lo = *(const u32x4 *)&sm.colmax[0][0][4 * sub], hi = *(const u32x4 *)&sm.colmax[0][1][4 * sub];
-#pragma unroll
-  for (int w = 1; w < kQuantWaves; ++w) {
-    lo = __builtin_elementwise_max(lo, *(const u32x4 *)&sm.colmax[w][0][4 * sub]);
-    hi = __builtin_elementwise_max(hi, *(const u32x4 *)&sm.colmax[w][1][4 * sub]);
+  {   // four lanes a column
+    const uint32_t *w = &sm.colmax[t >> 2][2 * (t & 3)];
+    const uint32_t e = e4m3_scale_byte(quad_max_u32(max(w[0], w[1])));
+    if ((t & 3) == 0) {
+      sm.inverse[t >> 2] = pow2_inverse(e);
+      scales[row0 + (t >> 2)] = pow2_scale(e);
+    }
   }
+  __syncthreads();
+  const f32x4 lo = *(const f32x4 *)&sm.inverse[8 * sub], hi = *(const f32x4 *)&sm.inverse[8 * sub + 4];
   const int piece = wave;   // 16 tokens
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const int col = 8 * sub + c;
-    const uint32_t e = e4m3_scale_byte(c < 4 ? lo[c & 3] : hi[c & 3]);
-    const float inv = pow2_inverse(e);
+    const float inv = c < 4 ? lo[c & 3] : hi[c & 3];
     *(uint32_t *)&sm.codes[(col ^ (sub >> 3)) * 128 + ((piece ^ (sub & 7)) << 4) + 4 * grp] =
         codes4(v[0][c] * inv, v[1][c] * inv, v[2][c] * inv, v[3][c] * inv);
-    if (wave == 0 && grp == 0) scales[row0 + col] = pow2_scale(e);
   }
   __syncthreads();
 #pragma unroll
