@@ -29,19 +29,17 @@ namespace {
 // and a column's four rows pack into one 4-byte piece of the transposed tile,
 // which goes through LDS to whole-line stores.
 //
-// Measured, 4096 x 18432 and x 4096 x 7168: 843 MB in 199 us, 4.2 TB/s; the
-// arithmetic, some 50 instructions an element, is 60% of that and overlaps the
-// loads of the CU's other workgroup only.  Stores that met half the banks made it
-// 225 us, every thread reducing the waves' column maxima for itself 212.
+// Measured, 4096 x 18432 and x 4096 x 7168: 843 MB in 168 us, 5.0 TB/s, a copy's
+// rate; 333 x 1024 and x 896 6 us.  What it took: no branch inside the unrolled
+// element loops (199 and 10.5 us with rows tested at their loads), transposed
+// stores that meet every bank once (225 us on half the banks), and the column
+// scales found once a workgroup (212 us by every thread).
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 512, kQuantWaves = kQuantThreads / 64, kLaneRows = 4;
 
 template <bool kBf16>
-__device__ __forceinline__ void load8(const void *p, int64_t idx, bool live, float (&v)[8]) {
-  if (!live) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] = 0.0f;
-  } else if (kBf16) {
+__device__ __forceinline__ void load8(const void *p, int64_t idx, float (&v)[8]) {
+  if (kBf16) {
     const u32x4 w = *(const u32x4 *)((const uint16_t *)p + idx);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -56,6 +54,15 @@ __device__ __forceinline__ void load8(const void *p, int64_t idx, bool live, flo
       v[4 + c] = hi[c];
     }
   }
+}
+
+// The values of rows past the last, loaded from it, are zero.
+__device__ __forceinline__ void clear_past(float (&v)[kLaneRows][8], int64_t row0, int64_t m0, int64_t m) {
+  if (m0 + kBlock <= m) return;
+#pragma unroll
+  for (int r = 0; r < kLaneRows; ++r)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[r][c] = row0 + r < m ? v[r][c] : 0.0f;
 }
 
 // E4M3 codes of four values already divided by their scale.
@@ -161,8 +168,8 @@ struct QuantArgs {
 // Everything that the products read, in one launch: the first workgroups
 // quantize a tile of dg and du each, the others a tile of x.  With fewer tiles
 // than CUs (kSplit) the tile's four results (dg or du, along the features or the
-// tokens) go to a workgroup each: 333 x 1024 took 15 us in one piece, its
-// arithmetic on 24 CUs.
+// tokens) go to a workgroup each (333 x 1024 in one piece: 15 us in the kernel's
+// first form, 11 in four, its arithmetic on 24 CUs).
 template <bool kBf16, bool kSplit>
 __global__ __launch_bounds__(kQuantThreads) void ffn_quant_kernel(const QuantArgs p) {
   __shared__ TokenTile sm;
@@ -174,23 +181,20 @@ __global__ __launch_bounds__(kQuantThreads) void ffn_quant_kernel(const QuantArg
     const int64_t m0 = (int64_t)(tile / across) * kBlock, k0 = (int64_t)(tile % across) * kBlock;
     float v[kLaneRows][8];
 #pragma unroll
-    for (int r = 0; r < kLaneRows; ++r) {
-      const int64_t row = m0 + lane_row + r;
-      load8<kBf16>(p.x, row * p.k + k0 + lane_col, row < p.m, v[r]);
-    }
+    for (int r = 0; r < kLaneRows; ++r) load8<kBf16>(p.x, min(m0 + lane_row + r, p.m - 1) * p.k + k0 + lane_col, v[r]);
+    clear_past(v, m0 + lane_row, m0, p.m);
     store_tokens(v, sm, p.xq, p.xs + m0 / kBlock * p.k, k0, m0, p.mpad);
     return;
   }
   const int tile = kSplit ? blockIdx.x >> 2 : blockIdx.x, across = (int)(p.f / kBlock);
   const int64_t m0 = (int64_t)(tile / across) * kBlock, f0 = (int64_t)(tile % across) * kBlock;
   const int64_t row0 = m0 + lane_row;
-  // one of the two gradients from dh, g, u
-  auto grad = [](bool gate, float h, float g, float u) {
-    // the reciprocal instruction is within one ulp; exp overflows to infinity
-    // for g below -88, where the sigmoid is 0 to fp32's precision
-    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
-    return gate ? h * u * (s * __builtin_fmaf(g, 1.0f - s, 1.0f)) : h * (g * s);
-  };
+  // the two gradients from dh, g, u: the reciprocal instruction is within one
+  // ulp; exp overflows to infinity for g below -88, where the sigmoid is 0 to
+  // fp32's precision
+  auto sigmoid = [](float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); };
+  auto grad_gate = [](float h, float g, float u, float s) { return h * u * (s * __builtin_fmaf(g, 1.0f - s, 1.0f)); };
+  auto grad_up = [](float h, float g, float s) { return h * (g * s); };
   auto along_rows = [&](const float (&v)[kLaneRows][8], bool gate) {
     store_rows(v, p.rq + (gate ? 0 : p.f) + f0 + lane_col, 2 * p.f,
                p.rs + (f0 + (gate ? 0 : p.f)) / kBlock * p.rs_stride, row0, p.m);
@@ -199,38 +203,43 @@ __global__ __launch_bounds__(kQuantThreads) void ffn_quant_kernel(const QuantArg
     store_tokens(v, sm, p.cq, p.cs + m0 / kBlock * p.cs_stride, (gate ? 0 : p.f) + f0, m0, p.mpad);
   };
   float hv[kLaneRows][8], gv[kLaneRows][8], uv[kLaneRows][8];
+  const bool split_gate = (blockIdx.x & 1) == 0, split_rows = (blockIdx.x & 2) == 0;
+  if (kSplit && (split_rows ? !p.rq : !p.cq)) return;
+#pragma unroll
+  for (int r = 0; r < kLaneRows; ++r) {
+    const int64_t idx = min(row0 + r, p.m - 1) * p.f + f0 + lane_col;
+    load8<kBf16>(p.dh, idx, hv[r]);
+    load8<kBf16>(p.g, idx, gv[r]);
+    if (!kSplit) load8<kBf16>(p.u, idx, uv[r]);
+  }
   if (kSplit) {
-    const bool gate = (blockIdx.x & 1) == 0, rows = (blockIdx.x & 2) == 0;
-    if (rows ? !p.rq : !p.cq) return;
+    if (split_gate) {
 #pragma unroll
-    for (int r = 0; r < kLaneRows; ++r) {
-      const bool live = row0 + r < p.m;
-      const int64_t idx = (row0 + r) * p.f + f0 + lane_col;
-      load8<kBf16>(p.dh, idx, live, hv[r]);
-      load8<kBf16>(p.g, idx, live, gv[r]);
-      load8<kBf16>(p.u, idx, live && gate, uv[r]);
+      for (int r = 0; r < kLaneRows; ++r) load8<kBf16>(p.u, min(row0 + r, p.m - 1) * p.f + f0 + lane_col, uv[r]);
+#pragma unroll
+      for (int r = 0; r < kLaneRows; ++r)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) hv[r][c] = grad_gate(hv[r][c], gv[r][c], uv[r][c], sigmoid(gv[r][c]));
+    } else {
+#pragma unroll
+      for (int r = 0; r < kLaneRows; ++r)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) hv[r][c] = grad_up(hv[r][c], gv[r][c], sigmoid(gv[r][c]));
     }
-#pragma unroll
-    for (int r = 0; r < kLaneRows; ++r)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) hv[r][c] = grad(gate, hv[r][c], gv[r][c], uv[r][c]);
-    if (rows) along_rows(hv, gate); else along_tokens(hv, gate);
+    clear_past(hv, row0, m0, p.m);
+    if (split_rows) along_rows(hv, split_gate); else along_tokens(hv, split_gate);
     return;
   }
 #pragma unroll
-  for (int r = 0; r < kLaneRows; ++r) {
-    const bool live = row0 + r < p.m;
-    const int64_t idx = (row0 + r) * p.f + f0 + lane_col;
-    load8<kBf16>(p.dh, idx, live, hv[r]);
-    load8<kBf16>(p.g, idx, live, gv[r]);
-    load8<kBf16>(p.u, idx, live, uv[r]);
+  for (int r = 0; r < kLaneRows; ++r)
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float h = hv[r][c], g = gv[r][c];
-      hv[r][c] = grad(true, h, g, uv[r][c]);
-      gv[r][c] = grad(false, h, g, uv[r][c]);
+      const float h = hv[r][c], g = gv[r][c], s = sigmoid(g);
+      hv[r][c] = grad_gate(h, g, uv[r][c], s);
+      gv[r][c] = grad_up(h, g, s);
     }
-  }
+  clear_past(hv, row0, m0, p.m);
+  clear_past(gv, row0, m0, p.m);
   if (p.rq) {
     along_rows(hv, true);
     along_rows(gv, false);
