@@ -332,6 +332,22 @@ TilePlan input_plan(int64_t m, int64_t f, int64_t k) {
 TilePlan weight_plan(int64_t m, int64_t f, int64_t k) {
   return tile_plan(2 * f, k, kBigTile, (int)(tokens_padded(m) / kBlock), current_device_cus());
 }
+// dW's plan beside a dx in 128 x 128 tiles: up to three rounds of those, over few
+// tokens, cost less in dx's launch than a launch of 256 x 256 tiles after it.
+// Measured (us, one launch and two): 1 x 2048 x 1792 28 and 34, 64 x 1664 x 1664 24
+// and 32, 5 x 1536 x 3712 33 and 36, 1000 x 2048 x 2048 56 and 58; with ten
+// rounds, 2 x 5120 x 3968, 73 and 60.
+TilePlan paired_weight_plan(int64_t m, int64_t f, int64_t k) {
+  TilePlan wt = weight_plan(m, f, k);
+  const int64_t tiles_a = 2 * f / kMidTile, tiles_b = k / kMidTile;
+  const int cus = current_device_cus();
+  if (wt.big && tokens_padded(m) <= 8 * kBlock && tiles_a * tiles_b <= 3 * (int64_t)(cus > 0 ? cus : 256)) {
+    wt.big = false;
+    wt.tiles_a = (int)tiles_a;
+    wt.tiles_b = (int)tiles_b;
+  }
+  return wt;
+}
 
 }  // namespace
 
@@ -353,7 +369,9 @@ hipError_t launch_gated_ffn_backward(const void *dh, const void *x, const void *
                                      const uint8_t *wg, const float *wg_s, const uint8_t *wu, const float *wu_s,
                                      void *dx, void *dwg, void *dwu, bool out_bf16, int64_t m, int64_t f, int64_t k,
                                      void *workspace, hipStream_t stream) {
-  const TilePlan in = input_plan(m, f, k), wt = weight_plan(m, f, k);
+  const bool want_dx = dx && m > 0;
+  const TilePlan in = input_plan(m, f, k);
+  const TilePlan wt = want_dx && !in.big ? paired_weight_plan(m, f, k) : weight_plan(m, f, k);
   const FfnSpace ws = backward_space(m, f, k);
   const int64_t mpad = tokens_padded(m);
   const int cus = current_device_cus();
@@ -421,7 +439,6 @@ hipError_t launch_gated_ffn_backward(const void *dh, const void *x, const void *
   pw.a_stride = rows_padded(2 * f);
   pw.b_stride = k;
   pw.nkb = (int)(mpad / kBlock);
-  const bool want_dx = dx && m > 0;
   if (want_dx && dwg && !in.big && !wt.big) return launch_mid_pair(in, pi, wt, pw, out_bf16, stream);
   if (want_dx && dwg && in.big && wt.big) return launch_big_pair(in, pi, wt, pw, out_bf16, cus, stream);
   if (want_dx) {
