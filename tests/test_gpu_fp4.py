@@ -88,7 +88,8 @@ def _gemv_check(x, q, s, b, out, got):
 # whole steps; the ends of the 16-row tiles on both sides; more rows than any tile
 @pytest.mark.parametrize("m,n,k", [(1, 1, 32), (1, 16, 64), (1, 1000, 96), (2, 17, 160), (1, 4096, 7168), (3, 1000, 1056),
                                    (13, 311, 4128), (16, 64, 512), (17, 33, 544), (32, 100, 2048), (40, 2048, 256),
-                                   (64, 129, 1024), (65, 48, 128), (200, 70, 352), (8, 18432, 512), (5, 40, 18432)])
+                                   (64, 129, 1024), (65, 48, 128), (200, 70, 352), (8, 18432, 512), (5, 40, 18432),
+                                   (32, 500, 512), (45, 20, 4128), (3, 20, 100032)])
 @pytest.mark.parametrize("x_type,out", [("bf16", "bf16"), ("f32", "f32")])
 def test_gemv_shapes(m, n, k, x_type, out):
     G.announce(f"fp4_gemv m={m} n={n} k={k} {x_type} -> {out}")

@@ -73,6 +73,30 @@ def test_gradients_of_any_size(scale):
     _check(acts, wg, wu, _run(acts, wg, wu, out_dtype=torch.float32), "f32")
 
 
+# both products in 256 x 256 tiles: dx's last round short by 56 workgroups, which
+# take two of dW's tiles first; and by 168 after two full rounds, dW's tiles being
+# the longer ones.  A dx of 128 x 128 tiles beside three rounds of dW's, and a dW
+# too large for that.
+@pytest.mark.parametrize("m,f,k", [(1600, 2304, 7040), (3000, 512, 12800), (70, 1792, 3456), (3, 5120, 3968)])
+def test_many_tiles(m, f, k):
+    """Sampled rows of dx, and sampled features and columns of dW."""
+    G.announce(f"gated_ffn_backward m={m} f={f} k={k}")
+    (dh, x, g, u), wg, wu = _inputs(m, f, k)
+    got = [U.values(t) for t in _run((dh, x, g, u), wg, wu)]
+    dh, x, g, u = (t.float().double().numpy() for t in (dh, x, g, u))
+    rng = np.random.default_rng(0)
+    rows = np.unique(np.r_[0, m - 1, rng.integers(m, size=40)])
+    dg, du = (ffn.quantize_rows(v) for v in ffn.activation_grads(dh[rows], g[rows], u[rows]))
+    want = dg @ ffn.weight(*wg) + du @ ffn.weight(*wu)
+    assert U.rel_error(got[0][rows], want) <= U.REL["bf16"] + 3 / 8 / np.sqrt(dg.size)
+    feats = np.unique(np.r_[0, f - 1, rng.integers(f, size=40)])
+    cols = np.unique(np.r_[0, k - 1, rng.integers(k, size=600)])
+    xq = ffn.quantize_tokens(x[:, cols])
+    for have, v in zip(got[1:], ffn.activation_grads(dh[:, feats], g[:, feats], u[:, feats])):
+        want = ffn.quantize_tokens(v).T @ xq
+        assert U.rel_error(have[np.ix_(feats, cols)], want) <= U.REL["bf16"] + 3 / 8 / np.sqrt(v.size)
+
+
 def test_parts_and_zero_gradients():
     acts, wg, wu = _inputs(70, 256, 384)
     dx, dwg, dwu = _run(acts, wg, wu)
