@@ -41,7 +41,7 @@ def _check(x, wg, wu, fmt, out, got, rows=None):
 
 # one row; sixteen and seventeen; the ends of 16-, 32-, 64- and 256-row tiles;
 # features that are not a multiple of 16, 64 or 128, one feature; one K block,
-# odd numbers of them, and the longest K that keeps scales in tables
+# odd numbers of them, and a long K
 SHAPES = [(1, 128, 128), (1, 2300, 1024), (2, 1, 256), (3, 130, 384), (8, 4096, 512), (15, 333, 640), (16, 256, 512),
           (17, 129, 1152), (31, 700, 256), (33, 64, 128), (64, 1000, 768), (65, 257, 512), (127, 384, 640),
           (128, 128, 1024), (200, 1111, 384), (257, 640, 128), (300, 513, 2048), (513, 260, 896), (5, 300, 20608)]
@@ -78,6 +78,20 @@ def test_dense_block_sampled_rows(m, f, k):
     got = fb.gated_ffn(x.to(G.device()), U.gpu(wg[0]), U.gpu(wg[1]), U.gpu(wu[0]), U.gpu(wu[1]), save=True)
     rows = np.unique(np.concatenate([[0, m - 1], np.random.default_rng(0).integers(0, m, 6)]))
     _check(x, wg, wu, None, "bf16", got, rows)
+
+
+# more 256 x 256 tiles than CUs; features in whole vectors, and not
+@pytest.mark.parametrize("f", [2304, 2309])
+@pytest.mark.parametrize("fmt,out", [(None, "bf16"), ("ue8m0", "bf16"), (None, "f32"), ("ue8m0", "f32")])
+def test_many_tiles_sampled_rows(f, fmt, out):
+    m, k = 4000, 512
+    G.announce(f"gated_ffn m={m} f={f} k={k} {fmt} -> {out}")
+    x, wg, wu = _inputs(m, f, k)
+    args = (x.to(G.device()), U.gpu(wg[0]), U.gpu(wg[1]), U.gpu(wu[0]), U.gpu(wu[1]), fmt, U.TYPES[out])
+    got = fb.gated_ffn(*args, save=True)
+    rows = np.unique(np.r_[0, 255, 256, 3839, 3840, m - 1, np.random.default_rng(0).integers(0, m, 24)])
+    _check(x, wg, wu, fmt, out, got, rows)
+    assert torch.equal(fb.gated_ffn(*args), got[0])
 
 
 @pytest.mark.parametrize("m,f,k", [(1, 129, 128), (16, 45, 256), (50, 77, 128), (129, 259, 256), (260, 1, 128)])
