@@ -30,7 +30,8 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_gate_s: torch.Tensor, w_u
     ``x`` [..., K] bf16 or fp32, quantized as ``act_quant(x, 128, scale_fmt)``;
     both weights [F, K] with their block scales.  Returns ``h`` [..., F] in
     ``out_dtype``, or with ``save`` the tuple ``(h, g, u)``: what
-    ``gated_ffn_backward`` takes.
+    ``gated_ffn_backward`` takes.  Autograd does not see the call: ``GatedFFN``
+    is the differentiable form.
     """
     return _ffn_lib.ext().gated_ffn(x, w_gate, w_gate_s, w_up, w_up_s, _format(scale_fmt), _out(out_dtype), save)
 
@@ -51,12 +52,30 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor, u: to
                                              weight_grad)
 
 
+class _FirstOrder(torch.autograd.Function):
+    """Hands gradients on; differentiating them raises.
+
+    They come from the native kernels without a graph: without this, a backward
+    pass with ``create_graph`` would take them for constants.
+    """
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return grads
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("GatedFFN has no second-order gradients: its backward pass is not differentiable")
+
+
 class _GatedFFNFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, scale_fmt):
+    def forward(ctx, x, w_gate, w_up, scale_fmt, save):
         wg, wg_s = weight_quant(w_gate.detach())
         wu, wu_s = weight_quant(w_up.detach())
         x = x.contiguous()
+        if not save:   # g and u need not be stored
+            return gated_ffn(x, wg, wg_s, wu, wu_s, scale_fmt, x.dtype)
         h, g, u = gated_ffn(x, wg, wg_s, wu, wu_s, scale_fmt, x.dtype, save=True)
         ctx.save_for_backward(x, g, u, wg, wg_s, wu, wu_s)
         return h
@@ -65,9 +84,11 @@ class _GatedFFNFunction(torch.autograd.Function):
     def backward(ctx, dh):
         weight_grad = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
         x, *saved = ctx.saved_tensors
-        dx, dwg, dwu = gated_ffn_backward(dh.contiguous(), x, *saved, out_dtype=x.dtype,
-                                          input_grad=ctx.needs_input_grad[0], weight_grad=weight_grad)
-        return dx, dwg, dwu, None
+        grads = gated_ffn_backward(dh.contiguous(), x, *saved, out_dtype=x.dtype,
+                                   input_grad=ctx.needs_input_grad[0], weight_grad=weight_grad)
+        if torch.is_grad_enabled():   # create_graph; dh need not have a graph for the gradients to depend on x and the weights
+            grads = _FirstOrder.apply(torch.zeros((), requires_grad=True), *grads)
+        return *grads, None, None
 
 
 class GatedFFN(torch.nn.Module):
@@ -75,7 +96,8 @@ class GatedFFN(torch.nn.Module):
 
     Master weights ``w_gate``, ``w_up`` [F, K] are kept in ``dtype`` (bf16 or
     fp32) and quantized per 128 x 128 tile in every forward pass; activations and
-    gradients have the same dtype.
+    gradients have the same dtype.  First-order gradients only: differentiating
+    them, or forward-mode differentiation, raises.
     """
 
     def __init__(self, in_features: int, hidden_features: int, dtype: torch.dtype = torch.bfloat16, scale_fmt=None,
@@ -96,9 +118,8 @@ class GatedFFN(torch.nn.Module):
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
         x = x.to(self.w_gate.dtype)
-        if not torch.is_grad_enabled():   # g and u need not be stored
-            return gated_ffn(x.contiguous(), *weight_quant(self.w_gate), *weight_quant(self.w_up), self.scale_fmt, x.dtype)
-        return _GatedFFNFunction.apply(x, self.w_gate, self.w_up, self.scale_fmt)
+        # without gradients too: the function refuses a forward-mode tangent, a plain call would drop it
+        return _GatedFFNFunction.apply(x, self.w_gate, self.w_up, self.scale_fmt, torch.is_grad_enabled())
 
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, hidden_features={self.hidden_features}, "
