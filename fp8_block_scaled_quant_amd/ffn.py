@@ -52,6 +52,13 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor, u: to
                                              weight_grad)
 
 
+def _operand(t):
+    """``t`` as the library takes it, contiguous and 16-byte aligned: a contiguous
+    view (a piece of a flattened ``cat``, say) may start anywhere."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _FirstOrder(torch.autograd.Function):
     """Hands gradients on; differentiating them raises.
 
@@ -73,7 +80,7 @@ class _GatedFFNFunction(torch.autograd.Function):
     def forward(ctx, x, w_gate, w_up, scale_fmt, save):
         wg, wg_s = weight_quant(w_gate.detach())
         wu, wu_s = weight_quant(w_up.detach())
-        x = x.contiguous()
+        x = _operand(x)
         if not save:   # g and u need not be stored
             return gated_ffn(x, wg, wg_s, wu, wu_s, scale_fmt, x.dtype)
         h, g, u = gated_ffn(x, wg, wg_s, wu, wu_s, scale_fmt, x.dtype, save=True)
@@ -84,7 +91,7 @@ class _GatedFFNFunction(torch.autograd.Function):
     def backward(ctx, dh):
         weight_grad = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
         x, *saved = ctx.saved_tensors
-        grads = gated_ffn_backward(dh.contiguous(), x, *saved, out_dtype=x.dtype,
+        grads = gated_ffn_backward(_operand(dh), x, *saved, out_dtype=x.dtype,
                                    input_grad=ctx.needs_input_grad[0], weight_grad=weight_grad)
         if torch.is_grad_enabled():   # create_graph; dh need not have a graph for the gradients to depend on x and the weights
             grads = _FirstOrder.apply(torch.zeros((), requires_grad=True), *grads)

@@ -12,7 +12,7 @@ from fp8_block_scaled_quant_amd import ffn
 
 @torch.no_grad()
 def _forward(x, wg, wg_s, wu, wu_s, scale_fmt=None, out_dtype=torch.bfloat16, save=False):
-    assert x.is_contiguous()
+    assert x.is_contiguous() and x.data_ptr() % 16 == 0
     g, u = x.double() @ wg.T, x.double() @ wu.T
     out = [t.to(out_dtype) for t in (g * torch.sigmoid(g) * u, g, u)]
     return tuple(out) if save else out[0]
@@ -20,7 +20,7 @@ def _forward(x, wg, wg_s, wu, wu_s, scale_fmt=None, out_dtype=torch.bfloat16, sa
 
 @torch.no_grad()
 def _backward(dh, x, g, u, wg, wg_s, wu, wu_s, out_dtype=torch.bfloat16, input_grad=True, weight_grad=True):
-    assert dh.is_contiguous()
+    assert all(t.is_contiguous() and t.data_ptr() % 16 == 0 for t in (dh, x, g, u))
     dh, x, g, u = (t.double() for t in (dh, x, g, u))
     s = torch.sigmoid(g)
     dg, du = dh * u * s * (1 + g * (1 - s)), dh * g * s
@@ -94,3 +94,29 @@ def test_only_the_gradients_asked_for(module):
     x = _x()
     module(x).sum().backward()
     assert x.grad is not None
+
+
+def test_views_that_start_anywhere(module):
+    """x one element into a buffer; h joined behind one element, whose gradient is
+    then a contiguous view one element into another."""
+    x = _x(False)
+    shifted = torch.cat([torch.zeros(1), x.flatten()])[1:].view(5, 128).requires_grad_()
+    assert shifted.is_contiguous() and shifted.data_ptr() % 16
+    weights = torch.randn(5 * 128, generator=torch.Generator().manual_seed(2))
+    joined = torch.cat([torch.zeros(1), module(shifted).flatten()])
+    (joined * torch.cat([torch.zeros(1), weights])).sum().backward()
+    h, leaves = _reference(module, x)
+    (h.flatten() * weights).sum().backward()
+    for have, want in zip((shifted, module.w_gate, module.w_up), leaves):
+        torch.testing.assert_close(have.grad, want.grad, rtol=1e-4, atol=1e-4)
+    with torch.no_grad():
+        assert torch.equal(module(shifted), module(x))
+
+
+def test_views_that_are_not_contiguous(module):
+    x = torch.randn(128, 5).t().requires_grad_()
+    h = module(x)
+    h.t().contiguous().square().sum().backward()
+    ref, leaves = _reference(module, x)
+    ref.square().sum().backward()
+    torch.testing.assert_close(x.grad, leaves[0].grad, rtol=1e-4, atol=1e-4)
