@@ -120,8 +120,10 @@ __device__ __forceinline__ float clip_factor(const double *__restrict__ partials
   for (int i = threadIdx.x; i < n; i += 256) sum += partials[i];
   const float norm = (float)sqrt(block_sum(sum, lds));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-  const float f = max_norm / (norm + eps);
-  return f > 1.0f ? 1.0f : f;   // a NaN norm stays NaN
+  // compared before the division: 0 / 0 and infinity / infinity would be NaN,
+  // where nothing is to be clipped.  A NaN norm stays NaN.
+  const float bound = norm + eps;
+  return max_norm >= bound ? 1.0f : max_norm / bound;
 }
 
 __global__ __launch_bounds__(256) void clip_norm_kernel(const double *__restrict__ partials, int n,

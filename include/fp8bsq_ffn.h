@@ -128,13 +128,14 @@ FP8BSQ_API int fp4_gemv(const void *x, int x_dtype, const uint8_t *q, const uint
  *            where numel is 0), element counts >= 0, FP8BSQ_F32 or FP8BSQ_BF16.
  *            outs = NULL: the norm only.  outs[i] has grads[i]'s dtype and is
  *            grads[i] itself (clipped in place) or does not overlap any grad.
- *   max_norm, eps   >= 0.
+ *   max_norm, eps   >= 0; the factor is 1 where max_norm >= norm + eps, so also
+ *            for an infinite max_norm, and for max_norm = norm + eps = 0.
  *   norm     device float out, 4-byte aligned.
  *
  * Squares are summed in FP64 in a fixed order: equal calls give equal bits, and
  * no square of a finite gradient overflows.  A NaN among the gradients makes
- * the norm and all outputs NaN; an infinite norm gives the factor 0 (and NaN
- * where a gradient is infinite).
+ * the norm and all outputs NaN; an infinite norm above max_norm gives the factor
+ * 0 (and NaN where a gradient is infinite).
  */
 FP8BSQ_API int fp8bsq_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *numels,
                           const int32_t *dtypes, int64_t count, float max_norm, float eps, float *norm,
