@@ -191,9 +191,10 @@ __global__ __launch_bounds__(kQuantThreads) void ffn_quant_kernel(const QuantArg
   const int64_t row0 = m0 + lane_row;
   // the two gradients from dh, g, u: the reciprocal instruction is within one
   // ulp; exp overflows to infinity for g below -88, where the sigmoid is 0 to
-  // fp32's precision
+  // fp32's precision.  The slope meets u before h: h u may overflow where the
+  // slope is 0 (a closed gate), and their product would be NaN
   auto sigmoid = [](float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); };
-  auto grad_gate = [](float h, float g, float u, float s) { return h * u * (s * __builtin_fmaf(g, 1.0f - s, 1.0f)); };
+  auto grad_gate = [](float h, float g, float u, float s) { return h * (u * (s * __builtin_fmaf(g, 1.0f - s, 1.0f))); };
   auto grad_up = [](float h, float g, float s) { return h * (g * s); };
   auto along_rows = [&](const float (&v)[kLaneRows][8], bool gate) {
     store_rows(v, p.rq + (gate ? 0 : p.f) + f0 + lane_col, 2 * p.f,
