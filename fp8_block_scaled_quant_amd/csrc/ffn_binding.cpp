@@ -221,6 +221,12 @@ Tensor clip(const py::list &grads, const std::optional<py::list> &outs, double m
   check_status(fp8bsq_clip_grad_norm(in.data(), outs ? out.data() : nullptr, numels.data(), dtypes.data(),
                                      (int64_t)count, (float)max_norm, (float)eps, (float *)norm.data_ptr(),
                                      ws.data_ptr(), bytes, stream_of(device)));
+  // a tensor that autograd saved is seen to have changed, as after torch's own in-place operations
+  if (outs)
+    for (size_t i = 0; i < count; ++i) {
+      const Tensor &t = tensor_of(PyList_GET_ITEM(outs->ptr(), i));
+      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    }
   return norm;
 }
 
