@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "fp8bsq_ffn.h"
+#include "spans.h"
 
 namespace py = pybind11;
 using at::Tensor;
@@ -196,6 +197,9 @@ Tensor clip(const py::list &grads, const std::optional<py::list> &outs, double m
   std::vector<void *> out(outs ? count : 0);
   std::vector<int64_t> numels(count);
   std::vector<int32_t> dtypes(count);
+  std::vector<c10::TensorImpl *> changed(out.size());
+  std::vector<fp8bsq::Span> spans;
+  if (in_place) spans.reserve(count);
   for (size_t i = 0; i < count; ++i) {
     const Tensor &t = tensor_of(PyList_GET_ITEM(grads.ptr(), i));
     require_gpu(t, device);
@@ -204,16 +208,19 @@ Tensor clip(const py::list &grads, const std::optional<py::list> &outs, double m
     in[i] = t.data_ptr();
     numels[i] = t.numel();
     if (!outs) continue;
-    if (in_place) {
-      out[i] = t.data_ptr();
-      continue;
+    const Tensor &o = in_place ? t : tensor_of(PyList_GET_ITEM(outs->ptr(), i));
+    if (!in_place) {
+      require_gpu(o, device);
+      if (o.sizes() != t.sizes() || o.scalar_type() != t.scalar_type())
+        value("out must match the gradients' number, shapes and dtypes");
     }
-    const Tensor &o = tensor_of(PyList_GET_ITEM(outs->ptr(), i));
-    require_gpu(o, device);
-    if (o.sizes() != t.sizes() || o.scalar_type() != t.scalar_type())
-      value("out must match the gradients' number, shapes and dtypes");
     out[i] = o.data_ptr();
+    if (out[i] == in[i] && numels[i])
+      spans.push_back({(uintptr_t)in[i], (uintptr_t)in[i] + (uintptr_t)numels[i] * (dtypes[i] == FP8BSQ_F32 ? 4 : 2)});
+    changed[i] = o.is_inference() ? nullptr : o.unsafeGetTensorImpl();
   }
+  // a shared weight's gradient listed twice: two workgroups would scale it, at once
+  if (fp8bsq::overlapping(std::move(spans))) value("gradients that are clipped in place must not overlap");
   const c10::DeviceGuard guard(device);
   const Tensor norm = empty({}, at::kFloat, device);
   const size_t bytes = fp8bsq_clip_grad_norm_workspace((int64_t)count);
@@ -222,11 +229,8 @@ Tensor clip(const py::list &grads, const std::optional<py::list> &outs, double m
                                      (int64_t)count, (float)max_norm, (float)eps, (float *)norm.data_ptr(),
                                      ws.data_ptr(), bytes, stream_of(device)));
   // a tensor that autograd saved is seen to have changed, as after torch's own in-place operations
-  if (outs)
-    for (size_t i = 0; i < count; ++i) {
-      const Tensor &t = tensor_of(PyList_GET_ITEM(outs->ptr(), i));
-      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-    }
+  for (c10::TensorImpl *t : changed)
+    if (t) t->bump_version();
   return norm;
 }
 

@@ -19,9 +19,10 @@ def clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6) -> torch
     their common 2-norm, which is returned (0-dim float32, before clipping).
 
     ``grads``: contiguous bf16/fp32 tensors on one GPU, or one tensor; views at
-    any offset are fine.  They are clipped in place, or into ``out`` (tensors of
-    the same shapes and dtypes that overlap no gradient).  A NaN gradient makes
-    the norm and every result NaN.
+    any offset are fine.  They are clipped in place, and then may not overlap (the
+    same tensor twice raises), or into ``out``: tensors of the same shapes and
+    dtypes that overlap neither each other nor any gradient (not checked).  A NaN
+    gradient makes the norm and every result NaN.
     """
     if not max_norm >= 0.0 or not eps >= 0.0:
         raise ValueError("max_norm and eps must not be negative")

@@ -127,7 +127,9 @@ FP8BSQ_API int fp4_gemv(const void *x, int x_dtype, const uint8_t *q, const uint
  *            the call: device pointers (aligned to their elements, NULL allowed
  *            where numel is 0), element counts >= 0, FP8BSQ_F32 or FP8BSQ_BF16.
  *            outs = NULL: the norm only.  outs[i] has grads[i]'s dtype and is
- *            grads[i] itself (clipped in place) or does not overlap any grad.
+ *            grads[i] itself (clipped in place, then apart from all other
+ *            grads) or does not overlap any grad; outs do not overlap.  This is
+ *            not checked.
  *   max_norm, eps   >= 0; the factor is 1 where max_norm >= norm + eps, so also
  *            for an infinite max_norm, and for max_norm = norm + eps = 0.
  *   norm     device float out, 4-byte aligned.
