@@ -22,6 +22,10 @@
 namespace fp8bsq {
 namespace {
 
+// A launch's table: 8 KB of kernel arguments.  The runtime takes the segment's
+// size from the code object; the tests fill a table to its last entry, eagerly and
+// replayed from a graph.  240 tensors take 12 us a call so, and 27 in three tables
+// of 96 (under 4 KB each): a table more is a pair of launches more.
 constexpr int kTableTensors = 256;
 constexpr int kChunk = 16384;       // elements
 constexpr int kClipBlocks = 1024;   // workgroups (and partials) per table, at most
@@ -35,6 +39,7 @@ struct Table {
   int32_t count;
   int64_t chunks;
 };
+static_assert(sizeof(Table) <= 8448, "no kernel argument segment larger than the tested one");
 
 // The tensor that a chunk belongs to: the last one whose first chunk is not
 // beyond it (tensors without elements have no chunk).  A wave holds all first
