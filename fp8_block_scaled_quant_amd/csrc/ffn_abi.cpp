@@ -1,6 +1,7 @@
 // C ABI of the feed-forward operators: argument validation, workspace layout
-// and dispatch.  Every check runs before any HIP call, so a rejected call
-// queues nothing.
+// and dispatch.  Every check runs before anything is queued; the one of a
+// workspace's size asks the runtime for the current device's compute units, by
+// which the products are planned.
 #include <stddef.h>
 #include <stdint.h>
 
@@ -40,12 +41,14 @@ int fp8_gated_ffn(const void *x, int x_dtype, int scale_fmt, const uint8_t *w_ga
   if (scale_fmt != FP8BSQ_SCALE_NONE && scale_fmt != FP8BSQ_SCALE_UE8M0) return FP8BSQ_EINVAL;
   if (k % 128 != 0) return FP8BSQ_ESHAPE;
   if (m == 0 || f == 0) return FP8BSQ_OK;
-  if (!x || !w_gate || !w_gate_s || !w_up || !w_up_s || !h || !workspace || !g != !u) return FP8BSQ_EINVAL;
+  if (!x || !w_gate || !w_gate_s || !w_up || !w_up_s || !h || !g != !u) return FP8BSQ_EINVAL;
+  // no workspace holds such sizes: its size was answered with 0
+  if (!ffn_sizes_ok(m, f, k)) return FP8BSQ_ERANGE;
+  if (!workspace) return FP8BSQ_EINVAL;
   const uintptr_t out = size_of(out_dtype);
   if (!aligned(x, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(w_gate_s, 4) ||
       !aligned(w_up_s, 4) || !aligned(h, out) || !aligned(g, out) || !aligned(u, out) || !aligned(workspace, 256))
     return FP8BSQ_EALIGN;
-  if (!ffn_sizes_ok(m, f, k)) return FP8BSQ_ERANGE;
   if (workspace_bytes < fp8bsq::gated_space(m, f, k).bytes) return FP8BSQ_ESCRATCH;
   return launch_status(fp8bsq::launch_gated_ffn(x, x_dtype == FP8BSQ_BF16, scale_fmt == FP8BSQ_SCALE_UE8M0, w_gate,
                                                 w_gate_s, w_up, w_up_s, h, g, u, out_dtype == FP8BSQ_BF16, m, f, k,
@@ -76,13 +79,13 @@ int fp8_gated_ffn_backward(const void *dh, const void *x, const void *g, const v
                                                            out_bf16, 0, f, k, nullptr, st));
   }
   if (!dx && !dw_gate) return FP8BSQ_OK;
-  if (!dh || !g || !u || !workspace || (dx && (!w_gate || !w_gate_s || !w_up || !w_up_s)) || (dw_gate && !x))
-    return FP8BSQ_EINVAL;
+  if (!dh || !g || !u || (dx && (!w_gate || !w_gate_s || !w_up || !w_up_s)) || (dw_gate && !x)) return FP8BSQ_EINVAL;
+  if (!ffn_sizes_ok(m, f, k)) return FP8BSQ_ERANGE;
+  if (!workspace) return FP8BSQ_EINVAL;
   if (!aligned(dh, 16) || !aligned(g, 16) || !aligned(u, 16) || !aligned(x, 16) || !aligned(w_gate, 16) ||
       !aligned(w_up, 16) || !aligned(w_gate_s, 4) || !aligned(w_up_s, 4) || !aligned(dx, 16) ||
       !aligned(dw_gate, 16) || !aligned(dw_up, 16) || !aligned(workspace, 256))
     return FP8BSQ_EALIGN;
-  if (!ffn_sizes_ok(m, f, k)) return FP8BSQ_ERANGE;
   if (workspace_bytes < fp8bsq::backward_space(m, f, k).bytes) return FP8BSQ_ESCRATCH;
   return launch_status(fp8bsq::launch_gated_ffn_backward(dh, x, g, u, in_bf16, w_gate, w_gate_s, w_up, w_up_s, dx,
                                                          dw_gate, dw_up, out_bf16, m, f, k, workspace, st));

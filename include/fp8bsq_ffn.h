@@ -10,13 +10,19 @@
  * synchronizing, no allocation, fp8bsq_status codes, every argument checked
  * before any HIP call, empty outputs answered with FP8BSQ_OK before any pointer
  * is looked at, finite inputs (NaN and Inf give unspecified but memory-safe
- * outputs unless an entry point says otherwise).  Two additions:
+ * outputs unless an entry point says otherwise).  Additions:
  *
  *  - A workspace is device memory of at least the size that the entry point's
- *    ..._workspace function gives for the same sizes, 256-byte aligned, with no
- *    initial contents required, in use until the queued work has finished.  A
- *    smaller one is FP8BSQ_ESCRATCH.  Calls that share one workspace must not
- *    overlap.
+ *    ..._workspace function gives for the same sizes with the same device
+ *    current, 256-byte aligned, with no initial contents required, in use until
+ *    the queued work has finished.  A smaller one is FP8BSQ_ESCRATCH.  Calls that
+ *    share one workspace must not overlap.
+ *  - That size follows from how a product is planned for the device's compute
+ *    units, for which the runtime is asked: a workspace's size is the one argument
+ *    whose check makes HIP calls (it queues nothing).
+ *  - The ..._workspace functions answer 0 for sizes that the call refuses; the
+ *    call says FP8BSQ_ERANGE or FP8BSQ_ESHAPE then, before it looks at the
+ *    workspace.
  *  - fp8bsq_strerror (libfp8bsq.so) describes the status codes.
  */
 #ifndef FP8BSQ_FFN_H
