@@ -417,13 +417,23 @@ hipError_t launch_gemv(GemvArgs a, hipStream_t stream) {
 
 hipError_t launch_fp4_weight_quant(const void *w, bool w_bf16, int64_t n, int64_t k, uint8_t *q, uint8_t *s,
                                    hipStream_t stream) {
+  // a launch has fewer than 2^32 threads, and more are dropped without an error:
+  // 2^34 weights each
+  constexpr int64_t kMost = (int64_t)1 << 29;
   const int64_t ngroups = n * (k / kGroup);
-  const dim3 grid((unsigned)((4 * ngroups + 255) / 256)), block(256);
-  if (w_bf16)
-    hipLaunchKernelGGL(fp4_weight_quant_kernel<true>, grid, block, 0, stream, w, ngroups, (uint32_t *)q, s);
-  else
-    hipLaunchKernelGGL(fp4_weight_quant_kernel<false>, grid, block, 0, stream, w, ngroups, (uint32_t *)q, s);
-  return hipGetLastError();
+  for (int64_t at = 0; at < ngroups; at += kMost) {
+    const int64_t part = min(ngroups - at, kMost);
+    const dim3 grid((unsigned)((4 * part + 255) / 256)), block(256);
+    const uint8_t *from = (const uint8_t *)w + at * kGroup * (w_bf16 ? 2 : 4);
+    uint32_t *codes = (uint32_t *)q + at * (kGroup / 8);
+    if (w_bf16)
+      hipLaunchKernelGGL(fp4_weight_quant_kernel<true>, grid, block, 0, stream, from, part, codes, s + at);
+    else
+      hipLaunchKernelGGL(fp4_weight_quant_kernel<false>, grid, block, 0, stream, from, part, codes, s + at);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_fp4_gemv(const void *x, bool x_bf16, const uint8_t *q, const uint8_t *s, const void *bias,
