@@ -10,7 +10,11 @@
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;         // per-dimension limit of the launch grids
+constexpr int64_t kMaxDim = (int64_t)1 << 31;
+// A launch has fewer than 2^32 threads along an axis, and more are dropped without
+// an error: the matrix-vector product's workgroups have up to 1024 for 144 rows of a
+// weight of so many.
+constexpr int64_t kMaxGemvN = 144 * (((int64_t)1 << 22) - 1);
 constexpr int64_t kMaxRows = (int64_t)65535 * 16;     // grid.y limit of the smallest row tile
 constexpr int64_t kMaxFeatures = (int64_t)1 << 21;    // features and K of the feed-forward block
 constexpr int64_t kMaxGemvK = (int64_t)1 << 27;       // 16 rows of codes within 32-bit offsets
@@ -112,7 +116,7 @@ int fp4_gemv(const void *x, int x_dtype, const uint8_t *q, const uint8_t *s, con
   if (!x || !q || !s || !y) return FP8BSQ_EINVAL;
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(bias, size_of(y_dtype)) || !aligned(y, size_of(y_dtype)))
     return FP8BSQ_EALIGN;
-  if (m > kMaxRows || n >= kMaxDim || k > kMaxGemvK) return FP8BSQ_ERANGE;
+  if (m > kMaxRows || n > kMaxGemvN || k > kMaxGemvK) return FP8BSQ_ERANGE;
   return launch_status(fp8bsq::launch_fp4_gemv(x, x_dtype == FP8BSQ_BF16, q, s, bias, y, y_dtype == FP8BSQ_BF16, m,
                                                n, k, (hipStream_t)hip_stream));
 }

@@ -52,7 +52,8 @@ extern "C" {
  *   g, u         [m, f] out, of the same dtype, or both NULL: the values the
  *                backward pass takes.
  *   m, f, k      m, f >= 0; k >= 128, k % 128 == 0 (else FP8BSQ_ESHAPE; k = 0 is
- *                FP8BSQ_EINVAL).  m or f = 0: nothing to do.
+ *                FP8BSQ_EINVAL); m <= 65535 * 16, f, k <= 2^21 (else
+ *                FP8BSQ_ERANGE).  m or f = 0: nothing to do.
  *
  * g and u meet fp8_block_gemm's error bound; they are rounded once, from the
  * FP32 values that h is formed from.
@@ -81,7 +82,8 @@ FP8BSQ_API size_t fp8_gated_ffn_workspace(int64_t m, int64_t f, int64_t k);
  *   dw_gate, dw_up  [f, k] out, or both NULL: not computed (x is not read and
  *                may then be NULL).
  *                Outputs have dtype out_dtype and are 16-byte aligned.
- *   m, f, k      m, f, k >= 0, f and k multiples of 128 (else FP8BSQ_ESHAPE).
+ *   m, f, k      m, f, k >= 0, f and k multiples of 128 (else FP8BSQ_ESHAPE);
+ *                ranges as for fp8_gated_ffn.
  *                f = 0 or k = 0 is FP8BSQ_EINVAL.  m = 0: dw_gate and dw_up are
  *                set to zero, and nothing else is read or written.
  */
@@ -118,7 +120,8 @@ FP8BSQ_API int fp4_weight_quant(const void *w, int w_dtype, int64_t n, int64_t k
  *   bias     [n] of y's dtype, or NULL.
  *   y        [m, n] out, dtype y_dtype, aligned to its elements.
  *   m, n, k  m, n >= 0; k >= 32, k % 32 == 0 (else FP8BSQ_ESHAPE; k = 0 is
- *            FP8BSQ_EINVAL).
+ *            FP8BSQ_EINVAL); m <= 65535 * 16, n <= 144 * (2^22 - 1), k <= 2^27 (else
+ *            FP8BSQ_ERANGE).
  *
  * Every product x * w is exact (fp32 x included); sums are FP32.
  */

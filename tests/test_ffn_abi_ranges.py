@@ -25,3 +25,9 @@ def test_missing_and_small_workspaces_within_range(lib):
     for workspace, status in ((None, _lib.EINVAL), (P, _lib.ESCRATCH)):
         assert lib.fp8_gated_ffn(P, 1, 0, P, P, P, P, P, None, None, 1, 40, 128, 128, workspace, 0, None) == status
         assert lib.fp8_gated_ffn_backward(P, P, P, P, 1, P, P, P, P, P, P, P, 1, 40, 128, 128, workspace, 0, None) == status
+
+
+def test_fp4_gemv_out_of_range(lib):
+    """A weight row more than the threads of one launch reach."""
+    for m, n, k in ((1, 144 * ((1 << 22) - 1) + 1, 32), (65535 * 16 + 1, 8, 32), (1, 8, (1 << 27) + 32)):
+        assert lib.fp4_gemv(P, 1, P, P, None, P, 1, m, n, k, None) == _lib.ERANGE

@@ -1,5 +1,6 @@
-"""4-bit weights beyond what one launch can take in threads: 2^35 weights and some,
-sampled on both sides of where one launch ends and the next begins."""
+"""4-bit weights at what one launch can take in threads and beyond: the quantizer on
+2^35 weights and some, sampled on both sides of where one launch ends and the next
+begins, and the product with as many weight rows as it takes."""
 
 import numpy as np
 import pytest
@@ -40,3 +41,23 @@ def test_quantizer_past_2_to_the_35():
     for at in range(0, n, 1 << 16):
         same = (s[at:at + (1 << 16)] == scales).all(1) & (q[at:at + (1 << 16)] == codes).all(1)
         assert bool((same | marked[at:at + (1 << 16)]).all()), at
+
+
+def test_gemv_with_the_most_rows():
+    n, k = 144 * ((1 << 22) - 1), 32
+    G.announce(f"fp4_gemv 1 x {n} x {k}")
+    gen = torch.Generator(G.device()).manual_seed(1)
+    x = torch.randn(1, k, generator=gen, device=G.device()).bfloat16()
+    q = torch.zeros(n, k // 2, dtype=torch.uint8, device=G.device())
+    first = torch.randint(256, (1 << 20,), generator=gen, device=G.device(), dtype=torch.uint8)
+    for at in range(0, n, 1 << 20):
+        q[at:at + (1 << 20), 3] = first[:min(1 << 20, n - at)]
+    s = torch.full((n, 1), 127, dtype=torch.uint8, device=G.device())
+    y = fb.fp4_gemv(x, q, s, torch.float32)
+    byte = torch.arange(256)
+    values = torch.from_numpy(fp4.DECODE).float()
+    table = (values[byte & 15] * x[0, 6].float().cpu() + values[byte >> 4] * x[0, 7].float().cpu()).to(x.device)
+    for at in range(0, n, 1 << 20):   # two exact products: one rounding
+        want = table[first[:min(1 << 20, n - at)].long()]
+        got = y[0, at:at + (1 << 20)]
+        assert bool(((got - want).abs() <= 2.0 ** -23 * want.abs()).all()), at
