@@ -60,8 +60,8 @@ __global__ __launch_bounds__(256) void fp4_weight_quant_kernel(const void *__res
 }
 
 // ---------------------------------------------------------------------------
-// y = x W^T.  An E2M1 code times its power-of-two scale is exact in bf16, and
-// one instruction turns two codes and the scale into two bf16, so the group
+// y = x W^T.  An E2M1 code times its power-of-two scale is exact in bf16 (scale
+// bytes up to 252; 6 times a larger one overflows), and one instruction turns two codes and the scale into two bf16, so the group
 // scales cost nothing in the product and one FP32 accumulator runs through K.
 //
 // MFMA 16x16x32 with the weights as the 16-row operand and 16 rows of x as
@@ -100,7 +100,8 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) {   //
   return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
-// Eight fp32 as the sum of three bf16 each: the upper 16 bits of what is left.
+// Eight fp32 as the sum of three bf16 each: the upper 16 bits of what is left,
+// which ends at bf16's smallest value, 2^-133: exact from |x| = 2^-110 on.
 __device__ __forceinline__ void split3(float (&r)[8], u32x4 (&parts)[3]) {
 #pragma unroll
   for (int q = 0; q < 3; ++q) {

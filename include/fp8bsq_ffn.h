@@ -116,14 +116,17 @@ FP8BSQ_API int fp4_weight_quant(const void *w, int w_dtype, int64_t n, int64_t k
  *
  *   x        [m, k] activations, dtype x_dtype, 16-byte aligned.
  *   q, s     as fp4_weight_quant writes them; q 16-byte aligned; scale bytes
- *            1..254.
+ *            0..252.  With 253 (which the quantizer writes for weights above
+ *            6 * 2^125 only) codes of 4 and 6 are beyond the weights' bf16, with
+ *            254 those from 2 on: such a row's results are infinite or NaN.
  *   bias     [n] of y's dtype, or NULL.
  *   y        [m, n] out, dtype y_dtype, aligned to its elements.
  *   m, n, k  m, n >= 0; k >= 32, k % 32 == 0 (else FP8BSQ_ESHAPE; k = 0 is
  *            FP8BSQ_EINVAL); m <= 65535 * 16, n <= 144 * (2^22 - 1), k <= 2^27 (else
  *            FP8BSQ_ERANGE).
  *
- * Every product x * w is exact (fp32 x included); sums are FP32.
+ * Every product x * w is exact, of fp32 x down to |x| = 2^-110; below, x loses
+ * what lies under 2^-133.  Sums are FP32.
  */
 FP8BSQ_API int fp4_gemv(const void *x, int x_dtype, const uint8_t *q, const uint8_t *s, const void *bias,
              void *y, int y_dtype, int64_t m, int64_t n, int64_t k, void *hip_stream);
