@@ -74,9 +74,9 @@ struct TokenTile {
   // [column][token]: 16-byte pieces swizzled by the column's 8, and columns 64
   // on in swapped pairs, so that a wave's stores, 16 columns apart by 8, touch
   // all banks once
-  uint8_t codes[128 * 128];
+  alignas(16) uint8_t codes[128 * 128];
   uint32_t colmax[128][kQuantWaves + 1];   // padded: a lane's eight columns, 8 apart, in different banks
-  float inverse[128];
+  alignas(16) float inverse[128];
 };
 
 // Quantize a tile's values v [4 rows][8 columns] along the rows (tokens) and
