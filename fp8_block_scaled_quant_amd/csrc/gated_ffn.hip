@@ -232,7 +232,7 @@ struct DecodePlan {
 
 DecodePlan decode_plan(int64_t m, int64_t f, int64_t k) {
   DecodePlan p;
-  if (m > kDecodeRows || m * k > 128 * 1024 || 8 * k >= ((int64_t)1 << 32)) return p;
+  if (m > kDecodeRows || m * k > 128 * 1024) return p;
   int cus = current_device_cus();
   if (cus <= 0) cus = 256;
   const int nkb = (int)(k / kBlock);
