@@ -1,7 +1,9 @@
 """Compile the HIP sources into the in-tree shared libraries ``libfp8bsq.so`` (the
 quantizers and the block-scaled GEMM) and ``libfp8bsq_ffn.so`` (the feed-forward
 operators, which call the first), and the latter's Python binding ``_ffn_ext.so``
-(host code over torch's headers).
+(host code over torch's headers, by g++).  The libraries need hipcc alone: run as
+a script where there is no torch or no g++, this file builds them and leaves the
+binding out.
 
 gfx950 only.  Packed-FP32 instruction selection is switched off for every HIP
 source, floating-point contraction is off unless a kernel asks for a fused
@@ -9,6 +11,7 @@ multiply-add explicitly, and no fast-math flag is used (the quantizer relies on
 IEEE division and exact fused multiply-adds).
 """
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -49,12 +52,17 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False, jobs: int = 4) -> str:
-    """Compile every source for gfx950 and link both libraries; returns ``libfp8bsq.so``'s path."""
+    """Compile every source for gfx950 and link both libraries and, with torch and g++, the binding.
+
+    Returns ``libfp8bsq.so``'s path.
+    """
     objdir = os.path.join(PKG_DIR, "_build")
     os.makedirs(objdir, exist_ok=True)
     cc = hipcc()
-    binding = (BINDING_SOURCE, subprocess.Popen(_binding_command(objdir, verbose), stdout=subprocess.PIPE,
-                                                stderr=subprocess.STDOUT))
+    missing = "torch" if importlib.util.find_spec("torch") is None else None if shutil.which("g++") else "g++"
+    if not missing:
+        binding = (BINDING_SOURCE, subprocess.Popen(_binding_command(objdir, verbose), stdout=subprocess.PIPE,
+                                                    stderr=subprocess.STDOUT))
     procs = []
     objs = {src: os.path.join(objdir, src + ".o") for src in SOURCES + FFN_SOURCES}
     # the slowest source first, so that the others compile beside it
@@ -72,6 +80,9 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
     _link(cc, [objs[s] for s in SOURCES], [], LIB_PATH, verbose)
     # found beside it at run time
     _link(cc, [objs[s] for s in FFN_SOURCES], ["-L", PKG_DIR, "-lfp8bsq", "-Wl,-rpath,$ORIGIN"], FFN_LIB_PATH, verbose)
+    if missing:
+        print(f"{missing} not found: the Python binding, {os.path.basename(BINDING_PATH)}, is not built", file=sys.stderr)
+        return LIB_PATH
     _drain([binding])
     from torch.utils import cpp_extension
     dirs = [arg for d in cpp_extension.library_paths() for arg in ("-L", d, "-Wl,-rpath," + d)]
@@ -87,7 +98,7 @@ def _binding_command(objdir, verbose):
 
     import torch
     from torch.utils import cpp_extension
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__",
+    cmd = [shutil.which("g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__",
            "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
            "-I", sysconfig.get_paths()["include"],
            *[arg for d in cpp_extension.include_paths("cuda") for arg in ("-isystem", d)],
