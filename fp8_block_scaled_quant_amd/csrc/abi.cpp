@@ -10,7 +10,12 @@
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;        // per-dimension limit of the launch grids
+constexpr int64_t kMaxDim = (int64_t)1 << 31;
+// A launch has fewer than 2^32 threads along an axis, and more are dropped without
+// an error: the fused product's workgroups have 1024 for 80 weight rows (the other
+// products' fewer for as many), the weight quantizers' 256 for 128 columns.
+constexpr int64_t kMaxGemmCols = 80 * (((int64_t)1 << 22) - 1);
+constexpr int64_t kMaxWeightCols = 128 * (((int64_t)1 << 24) - 1);
 constexpr int64_t kMaxGemmRows = (int64_t)65535 * 64; // grid.y limit of the GEMM launch
 
 bool aligned(const void *p, uintptr_t bytes) { return ((uintptr_t)p % bytes) == 0; }
@@ -47,7 +52,7 @@ int fp8_weight_dequant(const uint8_t *x, const float *s, int64_t m, int64_t n, i
   if (m == 0 || n == 0) return FP8BSQ_OK;
   if (!x || !s || !y) return FP8BSQ_EINVAL;
   if (!aligned(s, 4) || !aligned(y, y_dtype == FP8BSQ_F32 ? 4 : 2)) return FP8BSQ_EALIGN;
-  if (m >= kMaxDim || n >= kMaxDim || m * n >= ((int64_t)1 << 50)) return FP8BSQ_ERANGE;
+  if (m >= kMaxDim || n > kMaxWeightCols || m * n >= ((int64_t)1 << 50)) return FP8BSQ_ERANGE;
   return launch_status(fp8bsq::launch_weight_dequant(x, s, m, n, y, y_dtype == FP8BSQ_BF16,
                                                      (hipStream_t)hip_stream));
 }
@@ -61,7 +66,7 @@ int fp8_weight_quant(const void *x, int x_dtype, int64_t m, int64_t n, int block
   if (m == 0 || n == 0) return FP8BSQ_OK;
   if (!x || !y || !s) return FP8BSQ_EINVAL;
   if (!aligned(x, x_dtype == FP8BSQ_F32 ? 4 : 2) || !aligned(s, 4)) return FP8BSQ_EALIGN;
-  if (m >= kMaxDim || n >= kMaxDim || m * n >= ((int64_t)1 << 50)) return FP8BSQ_ERANGE;
+  if (m >= kMaxDim || n > kMaxWeightCols || m * n >= ((int64_t)1 << 50)) return FP8BSQ_ERANGE;
   if ((m + 127) / 128 > 65535) return FP8BSQ_ERANGE;   // grid.y
   return launch_status(fp8bsq::launch_weight_quant(x, x_dtype == FP8BSQ_BF16, m, n,
                                                    scale_fmt == FP8BSQ_SCALE_UE8M0, y, s,
@@ -83,7 +88,7 @@ int block_gemm_checked(const uint8_t *a, const float *a_s, const uint8_t *b, con
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_s, 4) || !aligned(b_s, 4) ||
       !aligned(c, 4))
     return FP8BSQ_EALIGN;
-  if (m > kMaxGemmRows || n >= kMaxDim || k >= kMaxDim) return FP8BSQ_ERANGE;
+  if (m > kMaxGemmRows || n > kMaxGemmCols || k >= kMaxDim) return FP8BSQ_ERANGE;
   const bool bf16 = c_dtype == FP8BSQ_BF16;
   const hipStream_t st = (hipStream_t)hip_stream;
   if (kernel == GemmKernel::kReference)
@@ -112,7 +117,7 @@ int fp8_block_gemm_reference(const uint8_t *a, const float *a_s, const uint8_t *
 
 size_t fp8_block_gemm_split_workspace(int64_t m, int64_t n, int64_t k) {
   if (m <= 0 || n <= 0 || k <= 0 || k % 128 != 0) return 0;   // rejected, or nothing to split
-  if (m > kMaxGemmRows || n >= kMaxDim || k >= kMaxDim) return 0;
+  if (m > kMaxGemmRows || n > kMaxGemmCols || k >= kMaxDim) return 0;
   return fp8bsq::block_gemm_split_bytes(m, n, k);
 }
 
@@ -128,7 +133,7 @@ int fp8_block_gemm_split(const uint8_t *a, const float *a_s, const uint8_t *b, c
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_s, 4) || !aligned(b_s, 4) ||
       !aligned(c, 4) || !aligned(workspace, 256))
     return FP8BSQ_EALIGN;
-  if (m > kMaxGemmRows || n >= kMaxDim || k >= kMaxDim) return FP8BSQ_ERANGE;
+  if (m > kMaxGemmRows || n > kMaxGemmCols || k >= kMaxDim) return FP8BSQ_ERANGE;
   return launch_status(fp8bsq::launch_block_gemm_split(
       a, a_s, b, b_s, c, c_dtype == FP8BSQ_BF16, m, n, k, (hipStream_t)hip_stream,
       scale_fmt == FP8BSQ_SCALE_UE8M0, workspace, workspace ? workspace_bytes : 0));
@@ -145,7 +150,7 @@ int fp8_block_gemm_split_noalloc(const uint8_t *a, const float *a_s, const uint8
   if (!a || !a_s || !b || !b_s || !c) return FP8BSQ_EINVAL;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_s, 4) || !aligned(b_s, 4) || !aligned(c, 4))
     return FP8BSQ_EALIGN;
-  if (m > kMaxGemmRows || n >= kMaxDim || k >= kMaxDim) return FP8BSQ_ERANGE;
+  if (m > kMaxGemmRows || n > kMaxGemmCols || k >= kMaxDim) return FP8BSQ_ERANGE;
   bool too_big = false;
   const int rc = launch_status(fp8bsq::launch_block_gemm_split_noalloc(
       a, a_s, b, b_s, c, c_dtype == FP8BSQ_BF16, m, n, k, (hipStream_t)hip_stream,
@@ -169,7 +174,7 @@ int fp8_act_quant_gemm(const void *x, int x_dtype, int scale_fmt, const uint8_t 
   if (product && (!aligned(b, 16) || !aligned(b_s, 4) || !aligned(c, 4) ||
                   !aligned(bias, c_dtype == FP8BSQ_F32 ? 4 : 2)))
     return FP8BSQ_EALIGN;
-  if (m > kMaxGemmRows || n >= kMaxDim || k >= kMaxDim) return FP8BSQ_ERANGE;
+  if (m > kMaxGemmRows || n > kMaxGemmCols || k >= kMaxDim) return FP8BSQ_ERANGE;
   if ((m * (k / 128) + 31) / 32 >= kMaxDim) return FP8BSQ_ERANGE;
   const hipStream_t st = (hipStream_t)hip_stream;
   const bool x_bf16 = x_dtype == FP8BSQ_BF16, ue8m0 = scale_fmt == FP8BSQ_SCALE_UE8M0;
