@@ -412,9 +412,9 @@ __global__ __launch_bounds__(kBigThreads) void e4m3_big_kernel(const TileArgs p)
 // last part to arrive, behind device-scope stores and a counter, the same split
 // took 4 us longer at 211 x 2300 x 7168: one workgroup then reads all parts.)
 //
-// Measured there: 18.5 us, and 4 for the sums; 56 blocks' latency in a third
-// each, and 33 MB of weights, are 7 us of it.  64 x 18432 x 7168: 75 us for 264
-// MB.
+// Measured there: 18.5 us, and 4 for the sums, for 72 tiles of 56 blocks, which
+// bring 132 MB to LDS (35 MB of them new).  64 x 18432 x 7168: 75-81 us for 264
+// MB, two rounds of tiles, the second an eighth full.
 // ---------------------------------------------------------------------------
 constexpr int kMidTile = 128, kMidThreads = 384, kMidSlots = 4;
 constexpr int kMidPartsMax = 16;

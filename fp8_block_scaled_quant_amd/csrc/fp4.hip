@@ -61,8 +61,9 @@ __global__ __launch_bounds__(256) void fp4_weight_quant_kernel(const void *__res
 
 // ---------------------------------------------------------------------------
 // y = x W^T.  An E2M1 code times its power-of-two scale is exact in bf16 (scale
-// bytes up to 252; 6 times a larger one overflows), and one instruction turns two codes and the scale into two bf16, so the group
-// scales cost nothing in the product and one FP32 accumulator runs through K.
+// bytes up to 252; 6 times a larger one overflows), and one instruction turns two
+// codes and the scale into two bf16, so the group scales cost nothing in the
+// product and one FP32 accumulator runs through K.
 //
 // MFMA 16x16x32 with the weights as the 16-row operand and 16 rows of x as
 // columns.  The order of K inside the operands is free as long as both agree:
@@ -82,8 +83,9 @@ __global__ __launch_bounds__(256) void fp4_weight_quant_kernel(const void *__res
 // workgroups reading the same part of them at once queue at a few L2 channels
 // (16 rows, 18432 x 28672: 137 us in one order for all).
 //
-// Measured, 18432 x 7168 (70.2 MB of codes and scales): one row 19 us, 3.7 TB/s;
-// 16 rows 23 us.  Fragments loaded straight to registers, 64 bytes of a row at a
+// Measured, 18432 x 7168 (70.2 MB of codes and scales): one row 19 us, 97 MB from
+// HBM at 5.2 TB/s (each step's 32 bytes of a row's scales bring their line again);
+// 16 rows 23-25 us.  Fragments loaded straight to registers, 64 bytes of a row at a
 // time, with x read by every wave, took 24 us for one row.
 // ---------------------------------------------------------------------------
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));

@@ -15,7 +15,7 @@
 // so they are read twice and written once.  396 M elements of bf16 (2.4 GB in
 // all) take 435 us, 5.5 TB/s; the second pass backwards, for what the last cache
 // still holds, took 440.  240 small tensors take the
-// kernels 4.3 and 4.9 us, latency, and the caller's own thread 14 a call.
+// kernels 4.3 and 4.9 us, latency, and the caller's own thread 15 a call.
 #include "ffn_launch.h"
 #include "device_common.h"
 
@@ -24,8 +24,8 @@ namespace {
 
 // A launch's table: 8 KB of kernel arguments.  The runtime takes the segment's
 // size from the code object; the tests fill a table to its last entry, eagerly and
-// replayed from a graph.  240 tensors take 12 us a call so, and 27 in three tables
-// of 96 (under 4 KB each): a table more is a pair of launches more.
+// replayed from a graph.  A table more is a pair of launches more: 240 tensors took
+// 27 us a call in three tables of 96, under 4 KB each, and 12 in one.
 constexpr int kTableTensors = 256;
 constexpr int kChunk = 16384;       // elements
 constexpr int kClipBlocks = 1024;   // workgroups (and partials) per table, at most
