@@ -50,7 +50,7 @@ typedef enum {
   FP8BSQ_EUNSUPPORTED = 3, /* block_size != 128 */
   FP8BSQ_EALIGN = 4,       /* a pointer lacks the alignment stated for it */
   FP8BSQ_ELAUNCH = 5,      /* the HIP runtime reported an error for the launch */
-  FP8BSQ_ERANGE = 6,       /* a size does not fit the kernels' 32-bit indexing limits */
+  FP8BSQ_ERANGE = 6,       /* a size does not fit the kernels' 32-bit indexing or launch limits */
   FP8BSQ_ESCRATCH = 7      /* the product needs more scratch than the static buffer holds */
 } fp8bsq_status;
 
