@@ -35,6 +35,17 @@ The feed-forward operators (``libfp8bsq_ffn.so``, declared in
 * ``fp4_weight_quant(w) -> (q, s)`` and ``fp4_gemv(x, q, s, out_dtype=torch.bfloat16, bias=None) -> y``:
   4-bit weights for the decode step;
 * ``clip_grad_norm(grads, max_norm, out=None, eps=1e-6) -> norm`` and ``grad_norm(grads) -> norm``.
+
+and the same block behind a router, whose tokens go to a few of many experts:
+
+* ``expert_sort(experts, num_experts) -> (offsets, rows, choices)``: the choices sorted by expert;
+* ``expert_dispatch(x, rows) -> y`` and ``expert_dispatch_quant(x, rows, scale_fmt=None) -> (y, s)``:
+  tokens' rows in that order;
+* ``expert_gated_ffn(a, a_s, offsets, w_gate, w_gate_s, w_up, w_up_s, out_dtype=torch.bfloat16) -> h``
+  and ``expert_gemm(a, a_s, offsets, b, b_s, out_dtype=torch.bfloat16) -> c``: each expert's rows with its own weights;
+* ``expert_combine(y, rows, weights=None) -> out`` and ``expert_combine_backward(dout, y, rows, weights, ...)``:
+  back to the tokens, weighted;
+* ``Experts``, an inference layer over them.
 """
 
 import ctypes
@@ -45,6 +56,8 @@ from . import _lib
 
 __all__ = ["act_quant", "weight_dequant", "weight_quant", "fp8_gemm", "act_quant_gemm", "Linear",
            "gated_ffn", "gated_ffn_backward", "GatedFFN", "fp4_weight_quant", "fp4_gemv", "clip_grad_norm", "grad_norm",
+           "ExpertSort", "expert_sort", "expert_dispatch", "expert_dispatch_quant", "expert_gated_ffn", "expert_gemm",
+           "expert_combine", "expert_combine_backward", "Experts",
            "Fp8Error", "library_path", "load_library"]
 
 Fp8Error = _lib.Fp8Error
@@ -245,6 +258,8 @@ def act_quant_gemm(x: torch.Tensor, b: torch.Tensor, b_s: torch.Tensor, scale_fm
     return c, y.view(torch.float8_e4m3fn), s
 
 
+from .experts import (ExpertSort, Experts, expert_combine, expert_combine_backward, expert_dispatch,  # noqa: E402
+                      expert_dispatch_quant, expert_gated_ffn, expert_gemm, expert_sort)
 from .ffn import GatedFFN, gated_ffn, gated_ffn_backward  # noqa: E402  (these use the functions above)
 from .fp4 import fp4_gemv, fp4_weight_quant  # noqa: E402
 from .grad_clip import clip_grad_norm, grad_norm  # noqa: E402

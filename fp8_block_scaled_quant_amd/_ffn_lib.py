@@ -13,7 +13,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8bsq_f
 
 # every symbol include/fp8bsq_ffn.h declares
 EXPORTS = ("fp8_gated_ffn", "fp8_gated_ffn_workspace", "fp8_gated_ffn_backward", "fp8_gated_ffn_backward_workspace",
-           "fp4_weight_quant", "fp4_gemv", "fp8bsq_clip_grad_norm", "fp8bsq_clip_grad_norm_workspace")
+           "fp4_weight_quant", "fp4_gemv", "fp8bsq_clip_grad_norm", "fp8bsq_clip_grad_norm_workspace",
+           "fp8bsq_expert_sort", "fp8bsq_expert_sort_workspace", "fp8bsq_expert_dispatch", "fp8_expert_dispatch_quant",
+           "fp8bsq_expert_combine", "fp8bsq_expert_combine_backward", "fp8_expert_gemm", "fp8_expert_gated_ffn")
 
 _LIB = None
 
@@ -35,13 +37,24 @@ def load_library(path: str = None) -> ctypes.CDLL:
     lib.fp4_weight_quant.argtypes = [vp, i32, i64, i64, vp, vp, vp]
     lib.fp4_gemv.argtypes = [vp, i32, vp, vp, vp, vp, i32, i64, i64, i64, vp]
     lib.fp8bsq_clip_grad_norm.argtypes = [vp, vp, vp, vp, i64, f32, f32, vp, vp, size, vp]
-    for name in ("fp8_gated_ffn", "fp8_gated_ffn_backward", "fp4_weight_quant", "fp4_gemv", "fp8bsq_clip_grad_norm"):
+    lib.fp8bsq_expert_sort.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp, size, vp]
+    lib.fp8bsq_expert_dispatch.argtypes = [vp, i32, vp, i64, i64, i64, vp, vp]
+    lib.fp8_expert_dispatch_quant.argtypes = [vp, i32, i32, vp, i64, i64, i64, vp, vp, vp]
+    lib.fp8bsq_expert_combine.argtypes = [vp, i32, vp, vp, i32, i64, i64, i64, vp, vp]
+    lib.fp8bsq_expert_combine_backward.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, vp, vp, vp]
+    lib.fp8_expert_gemm.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+    lib.fp8_expert_gated_ffn.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+    for name in ("fp8_gated_ffn", "fp8_gated_ffn_backward", "fp4_weight_quant", "fp4_gemv", "fp8bsq_clip_grad_norm",
+                 "fp8bsq_expert_sort", "fp8bsq_expert_dispatch", "fp8_expert_dispatch_quant", "fp8bsq_expert_combine",
+                 "fp8bsq_expert_combine_backward", "fp8_expert_gemm", "fp8_expert_gated_ffn"):
         getattr(lib, name).restype = i32
     for name in ("fp8_gated_ffn_workspace", "fp8_gated_ffn_backward_workspace"):
         getattr(lib, name).argtypes = [i64, i64, i64]
         getattr(lib, name).restype = size
     lib.fp8bsq_clip_grad_norm_workspace.argtypes = [i64]
-    lib.fp8bsq_clip_grad_norm_workspace.restype = size
+    lib.fp8bsq_expert_sort_workspace.argtypes = [i64, i64]
+    for name in ("fp8bsq_clip_grad_norm_workspace", "fp8bsq_expert_sort_workspace"):
+        getattr(lib, name).restype = size
     if path is None:
         _LIB = lib
     return lib

@@ -28,7 +28,8 @@ FFN_LIB_NAME = "libfp8bsq_ffn.so"
 FFN_LIB_PATH = os.path.join(PKG_DIR, FFN_LIB_NAME)
 
 SOURCES = ["abi.cpp", "act_quant.hip", "weight_dequant.hip", "weight_quant.hip", "block_gemm.hip"]
-FFN_SOURCES = ["ffn_abi.cpp", "gated_ffn.hip", "gated_ffn_backward.hip", "fp4.hip", "grad_clip.hip"]
+FFN_SOURCES = ["ffn_abi.cpp", "gated_ffn.hip", "gated_ffn_backward.hip", "fp4.hip", "grad_clip.hip",
+               "expert_sort.hip", "expert_rows.hip", "expert_gemm.hip"]
 BINDING_SOURCE = "ffn_binding.cpp"
 BINDING_PATH = os.path.join(PKG_DIR, "_ffn_ext.so")
 

@@ -5,8 +5,20 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "expert_launch.h"
 #include "ffn_launch.h"
 #include "fp8bsq_ffn.h"
+
+namespace fp8bsq {
+// Weak, so that this layer can be built over the other launchers alone.
+__attribute__((weak)) decltype(expert_sort_bytes) expert_sort_bytes;
+__attribute__((weak)) decltype(launch_expert_sort) launch_expert_sort;
+__attribute__((weak)) decltype(launch_expert_dispatch) launch_expert_dispatch;
+__attribute__((weak)) decltype(launch_expert_dispatch_quant) launch_expert_dispatch_quant;
+__attribute__((weak)) decltype(launch_expert_combine) launch_expert_combine;
+__attribute__((weak)) decltype(launch_expert_combine_backward) launch_expert_combine_backward;
+__attribute__((weak)) decltype(launch_expert_product) launch_expert_product;
+}  // namespace fp8bsq
 
 namespace {
 
@@ -27,6 +39,25 @@ int launch_status(hipError_t e) { return e == hipSuccess ? FP8BSQ_OK : FP8BSQ_EL
 // Rows reach the tile kernels by 32-bit offsets from their tile.
 bool ffn_sizes_ok(int64_t m, int64_t f, int64_t k) {
   return m > 0 && f > 0 && k > 0 && k % 128 == 0 && m <= kMaxRows && f <= kMaxFeatures && k <= kMaxFeatures;
+}
+
+// Choices and rows are counted in int32.
+bool choices_ok(int64_t tokens, int64_t top_k) { return tokens < kMaxDim && top_k < kMaxDim && tokens * top_k < kMaxDim; }
+
+// The products of the experts' rows: w1 null where there is one weight.
+int expert_product(const uint8_t *a, const float *a_s, const int32_t *offsets, bool gated, const uint8_t *w0,
+                   const float *w0_s, const uint8_t *w1, const float *w1_s, void *out, int out_dtype, int64_t rows,
+                   int64_t experts, int64_t f, int64_t k, void *hip_stream) {
+  if (rows < 0 || experts <= 0 || f < 0 || k <= 0 || !known_dtype(out_dtype)) return FP8BSQ_EINVAL;
+  if (k % 128 != 0) return FP8BSQ_ESHAPE;
+  if (rows == 0 || f == 0) return FP8BSQ_OK;
+  if (!a || !a_s || !offsets || !w0 || !w0_s || !out || (gated && (!w1 || !w1_s))) return FP8BSQ_EINVAL;
+  if (!aligned(a, 16) || !aligned(w0, 16) || !aligned(w1, 16) || !aligned(a_s, 4) || !aligned(w0_s, 4) ||
+      !aligned(w1_s, 4) || !aligned(offsets, 4) || !aligned(out, size_of(out_dtype)))
+    return FP8BSQ_EALIGN;
+  if (!ffn_sizes_ok(rows, f, k) || experts > fp8bsq::kMaxExperts) return FP8BSQ_ERANGE;
+  return launch_status(fp8bsq::launch_expert_product(a, a_s, offsets, w0, w0_s, w1, w1_s, out, out_dtype == FP8BSQ_BF16,
+                                                     rows, experts, f, k, (hipStream_t)hip_stream));
 }
 
 }  // namespace
@@ -140,6 +171,91 @@ int fp8bsq_clip_grad_norm(const void *const *grads, void *const *outs, const int
   if (workspace_bytes < fp8bsq::clip_workspace_bytes(count)) return FP8BSQ_ESCRATCH;
   return launch_status(fp8bsq::launch_clip_grad_norm(grads, outs, numels, dtypes, count, max_norm, eps, norm,
                                                      workspace, (hipStream_t)hip_stream));
+}
+
+size_t fp8bsq_expert_sort_workspace(int64_t n, int64_t num_experts) {
+  const bool ok = n >= 0 && n < kMaxDim && num_experts > 0 && num_experts <= fp8bsq::kMaxExperts;
+  return ok ? fp8bsq::expert_sort_bytes(n, num_experts) : 0;
+}
+
+int fp8bsq_expert_sort(const void *experts, int index_bytes, int64_t n, int64_t num_experts, int32_t *offsets,
+                       int32_t *rows, int32_t *choices, void *workspace, size_t workspace_bytes, void *hip_stream) {
+  if (n < 0 || num_experts <= 0 || (index_bytes != 4 && index_bytes != 8)) return FP8BSQ_EINVAL;
+  if (!offsets || (n > 0 && (!experts || !rows || !choices))) return FP8BSQ_EINVAL;
+  if (!aligned(experts, index_bytes) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(choices, 4) ||
+      !aligned(workspace, 256))
+    return FP8BSQ_EALIGN;
+  if (n >= kMaxDim || num_experts > fp8bsq::kMaxExperts) return FP8BSQ_ERANGE;
+  const size_t need = fp8bsq::expert_sort_bytes(n, num_experts);
+  if (need && !workspace) return FP8BSQ_EINVAL;
+  if (workspace_bytes < need) return FP8BSQ_ESCRATCH;
+  return launch_status(fp8bsq::launch_expert_sort(experts, index_bytes == 8, n, num_experts, offsets, rows, choices,
+                                                  workspace, (hipStream_t)hip_stream));
+}
+
+int fp8bsq_expert_dispatch(const void *x, int dtype, const int32_t *rows, int64_t tokens, int64_t top_k, int64_t h,
+                           void *y, void *hip_stream) {
+  if (tokens < 0 || top_k <= 0 || h < 0 || !known_dtype(dtype)) return FP8BSQ_EINVAL;
+  if (tokens == 0 || h == 0) return FP8BSQ_OK;
+  if (!x || !rows || !y) return FP8BSQ_EINVAL;
+  if (!aligned(x, size_of(dtype)) || !aligned(y, size_of(dtype)) || !aligned(rows, 4)) return FP8BSQ_EALIGN;
+  if (!choices_ok(tokens, top_k) || h > kMaxFeatures) return FP8BSQ_ERANGE;
+  return launch_status(
+      fp8bsq::launch_expert_dispatch(x, dtype == FP8BSQ_BF16, rows, tokens, top_k, h, y, (hipStream_t)hip_stream));
+}
+
+int fp8_expert_dispatch_quant(const void *x, int x_dtype, int scale_fmt, const int32_t *rows, int64_t tokens,
+                              int64_t top_k, int64_t h, uint8_t *y, float *s, void *hip_stream) {
+  if (tokens < 0 || top_k <= 0 || h < 0 || !known_dtype(x_dtype)) return FP8BSQ_EINVAL;
+  if (scale_fmt != FP8BSQ_SCALE_NONE && scale_fmt != FP8BSQ_SCALE_UE8M0) return FP8BSQ_EINVAL;
+  if (h % 128 != 0) return FP8BSQ_ESHAPE;
+  if (tokens == 0 || h == 0) return FP8BSQ_OK;
+  if (!x || !rows || !y || !s) return FP8BSQ_EINVAL;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(s, 4) || !aligned(rows, 4)) return FP8BSQ_EALIGN;
+  if (!choices_ok(tokens, top_k) || h > kMaxFeatures) return FP8BSQ_ERANGE;
+  return launch_status(fp8bsq::launch_expert_dispatch_quant(x, x_dtype == FP8BSQ_BF16, scale_fmt == FP8BSQ_SCALE_UE8M0,
+                                                            rows, tokens, top_k, h, y, s, (hipStream_t)hip_stream));
+}
+
+int fp8bsq_expert_combine(const void *y, int dtype, const int32_t *rows, const void *weights, int w_dtype,
+                          int64_t tokens, int64_t top_k, int64_t h, void *out, void *hip_stream) {
+  if (tokens < 0 || top_k <= 0 || h < 0 || !known_dtype(dtype) || !known_dtype(w_dtype)) return FP8BSQ_EINVAL;
+  if (tokens == 0 || h == 0) return FP8BSQ_OK;
+  if (!y || !rows || !out) return FP8BSQ_EINVAL;
+  if (!aligned(y, size_of(dtype)) || !aligned(out, size_of(dtype)) || !aligned(rows, 4) ||
+      !aligned(weights, size_of(w_dtype)))
+    return FP8BSQ_EALIGN;
+  if (!choices_ok(tokens, top_k) || h > kMaxFeatures) return FP8BSQ_ERANGE;
+  return launch_status(fp8bsq::launch_expert_combine(y, dtype == FP8BSQ_BF16, rows, weights, w_dtype == FP8BSQ_BF16,
+                                                     tokens, top_k, h, out, (hipStream_t)hip_stream));
+}
+
+int fp8bsq_expert_combine_backward(const void *dout, const void *y, int dtype, const int32_t *rows,
+                                   const void *weights, int w_dtype, int64_t tokens, int64_t top_k, int64_t h, void *dy,
+                                   void *dweights, void *hip_stream) {
+  if (tokens < 0 || top_k <= 0 || h < 0 || !known_dtype(dtype) || !known_dtype(w_dtype)) return FP8BSQ_EINVAL;
+  if (tokens == 0 || (!dy && !dweights) || (h == 0 && !dweights)) return FP8BSQ_OK;
+  if (!rows || (h > 0 && (!dout || (dweights && !y)))) return FP8BSQ_EINVAL;
+  const uintptr_t size = size_of(dtype);
+  if (!aligned(dout, size) || !aligned(y, size) || !aligned(dy, size) || !aligned(rows, 4) ||
+      !aligned(weights, size_of(w_dtype)) || !aligned(dweights, size_of(w_dtype)))
+    return FP8BSQ_EALIGN;
+  if (!choices_ok(tokens, top_k) || h > kMaxFeatures) return FP8BSQ_ERANGE;
+  return launch_status(fp8bsq::launch_expert_combine_backward(dout, y, dtype == FP8BSQ_BF16, rows, weights,
+                                                              w_dtype == FP8BSQ_BF16, tokens, top_k, h, dy, dweights,
+                                                              (hipStream_t)hip_stream));
+}
+
+int fp8_expert_gemm(const uint8_t *a, const float *a_s, const int32_t *offsets, const uint8_t *b, const float *b_s,
+                    void *c, int c_dtype, int64_t rows, int64_t num_experts, int64_t n, int64_t k, void *hip_stream) {
+  return expert_product(a, a_s, offsets, false, b, b_s, nullptr, nullptr, c, c_dtype, rows, num_experts, n, k, hip_stream);
+}
+
+int fp8_expert_gated_ffn(const uint8_t *a, const float *a_s, const int32_t *offsets, const uint8_t *w_gate,
+                         const float *w_gate_s, const uint8_t *w_up, const float *w_up_s, void *h, int out_dtype,
+                         int64_t rows, int64_t num_experts, int64_t f, int64_t k, void *hip_stream) {
+  return expert_product(a, a_s, offsets, true, w_gate, w_gate_s, w_up, w_up_s, h, out_dtype, rows, num_experts, f, k,
+                        hip_stream);
 }
 
 }  // extern "C"

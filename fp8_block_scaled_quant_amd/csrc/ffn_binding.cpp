@@ -63,6 +63,8 @@ std::vector<int64_t> with_last(const Tensor &t, int64_t last) {
   return shape;
 }
 
+py::object or_none(const Tensor &t) { return t.defined() ? py::cast(t) : py::object(py::none()); }
+
 struct Weight {
   const uint8_t *codes;
   const float *scales;
@@ -140,7 +142,6 @@ py::tuple gated_ffn_backward(const Tensor &dh, const Tensor &x, const Tensor &g,
         input_grad ? dx.data_ptr() : nullptr, weight_grad ? dwg.data_ptr() : nullptr,
         weight_grad ? dwu.data_ptr() : nullptr, out_dtype, m, f, k, ws.data_ptr(), bytes, stream_of(device)));
   }
-  auto or_none = [](const Tensor &t) { return t.defined() ? py::cast(t) : py::object(py::none()); };
   return py::make_tuple(or_none(dx), or_none(dwg), or_none(dwu));
 }
 
@@ -234,6 +235,180 @@ Tensor clip(const py::list &grads, const std::optional<py::list> &outs, double m
   return norm;
 }
 
+// ---------------------------------------------------------------------------
+// Experts
+// ---------------------------------------------------------------------------
+
+py::tuple expert_sort(const Tensor &experts, int64_t num_experts) {
+  const c10::Device device = experts.device();
+  require_gpu(experts, device);
+  const bool wide = experts.scalar_type() == at::kLong;
+  if (!wide && experts.scalar_type() != at::kInt) type("expert numbers must be int32 or int64");
+  if (experts.dim() == 0) value("expert numbers must be [..., top_k]");
+  if (num_experts <= 0) value("num_experts must be positive");
+  const int64_t n = experts.numel();
+  const c10::DeviceGuard guard(device);
+  const Tensor offsets = empty({num_experts + 1}, at::kInt, device), rows = empty(experts.sizes(), at::kInt, device),
+               choices = empty({n}, at::kInt, device);
+  const size_t bytes = fp8bsq_expert_sort_workspace(n, num_experts);
+  Tensor ws;
+  if (bytes) ws = workspace(bytes, device);
+  check_status(fp8bsq_expert_sort(experts.data_ptr(), wide ? 8 : 4, n, num_experts, (int32_t *)offsets.data_ptr(),
+                                  (int32_t *)rows.data_ptr(), (int32_t *)choices.data_ptr(),
+                                  bytes ? ws.data_ptr() : nullptr, bytes, stream_of(device)));
+  return py::make_tuple(offsets, rows, choices);
+}
+
+struct Choices {
+  const int32_t *rows;
+  int64_t tokens, top_k;
+};
+
+// rows [..., top_k]; a token's tensors have its leading dimensions.
+Choices choices_of(const Tensor &rows) {
+  if (rows.scalar_type() != at::kInt) type("rows must be int32, as expert_sort returns them");
+  if (rows.dim() == 0 || rows.size(-1) == 0) value("rows must be [..., top_k]");
+  return {(const int32_t *)rows.data_ptr(), rows.numel() / rows.size(-1), rows.size(-1)};
+}
+
+void require_tokens(const Tensor &x, const Tensor &rows) {
+  if (x.dim() == 0 || x.sizes().slice(0, x.dim() - 1) != rows.sizes().slice(0, rows.dim() - 1))
+    value("a token's tensors must have the leading dimensions of rows");
+}
+
+void require_sorted(const Tensor &y, const Choices &c) {
+  if (y.dim() != 2 || y.size(0) != c.tokens * c.top_k) value("sorted rows must be [T * top_k, H]");
+}
+
+// The weights' type; fp32 where there are none.
+int require_weights(const std::optional<Tensor> &weights, const Tensor &rows, c10::Device device) {
+  if (!weights) return FP8BSQ_F32;
+  require_gpu(*weights, device);
+  if (dtype_of(*weights) < 0) type("weights must be bf16 or fp32");
+  if (weights->sizes() != rows.sizes()) value("weights must have the shape of rows");
+  return dtype_of(*weights);
+}
+
+const void *data_or_null(const std::optional<Tensor> &t) { return t ? t->data_ptr() : nullptr; }
+
+Tensor expert_dispatch(const Tensor &x, const Tensor &rows) {
+  const c10::Device device = x.device();
+  for (const Tensor *t : {&x, &rows}) require_gpu(*t, device);
+  const int dtype = dtype_of(x);
+  if (dtype < 0) type("expert_dispatch takes bf16 or fp32 rows");
+  const Choices c = choices_of(rows);
+  require_tokens(x, rows);
+  const int64_t h = x.size(-1);
+  const c10::DeviceGuard guard(device);
+  const Tensor y = empty({c.tokens * c.top_k, h}, x.scalar_type(), device);
+  check_status(fp8bsq_expert_dispatch(x.data_ptr(), dtype, c.rows, c.tokens, c.top_k, h, y.data_ptr(), stream_of(device)));
+  return y;
+}
+
+py::tuple expert_dispatch_quant(const Tensor &x, const Tensor &rows, int scale_fmt) {
+  const c10::Device device = x.device();
+  for (const Tensor *t : {&x, &rows}) require_gpu(*t, device);
+  const int dtype = dtype_of(x);
+  if (dtype < 0) type("expert_dispatch_quant takes bf16 or fp32 rows");
+  const Choices c = choices_of(rows);
+  require_tokens(x, rows);
+  const int64_t h = x.size(-1), n = c.tokens * c.top_k;
+  if (h % 128 != 0) value("H must be a multiple of 128");
+  const c10::DeviceGuard guard(device);
+  const Tensor y = empty({n, h}, at::kFloat8_e4m3fn, device), s = empty({n, h / 128}, at::kFloat, device);
+  check_status(fp8_expert_dispatch_quant(x.data_ptr(), dtype, scale_fmt, c.rows, c.tokens, c.top_k, h,
+                                         (uint8_t *)y.data_ptr(), (float *)s.data_ptr(), stream_of(device)));
+  return py::make_tuple(y, s);
+}
+
+Tensor expert_combine(const Tensor &y, const Tensor &rows, const std::optional<Tensor> &weights) {
+  const c10::Device device = y.device();
+  for (const Tensor *t : {&y, &rows}) require_gpu(*t, device);
+  const int dtype = dtype_of(y);
+  if (dtype < 0) type("expert_combine takes bf16 or fp32 rows");
+  const Choices c = choices_of(rows);
+  require_sorted(y, c);
+  const int w_dtype = require_weights(weights, rows, device);
+  const int64_t h = y.size(1);
+  const c10::DeviceGuard guard(device);
+  const Tensor out = empty(with_last(rows, h), y.scalar_type(), device);
+  check_status(fp8bsq_expert_combine(y.data_ptr(), dtype, c.rows, data_or_null(weights), w_dtype, c.tokens, c.top_k, h,
+                                     out.data_ptr(), stream_of(device)));
+  return out;
+}
+
+py::tuple expert_combine_backward(const Tensor &dout, const Tensor &y, const Tensor &rows,
+                                  const std::optional<Tensor> &weights, bool row_grad, bool weight_grad) {
+  const c10::Device device = dout.device();
+  for (const Tensor *t : {&dout, &y, &rows}) require_gpu(*t, device);
+  const int dtype = dtype_of(dout);
+  if (dtype < 0 || dtype_of(y) != dtype) type("dout and y must both be bf16 or both fp32");
+  const Choices c = choices_of(rows);
+  require_tokens(dout, rows);
+  require_sorted(y, c);
+  if (y.size(1) != dout.size(-1)) value("dout and y must have rows of one length");
+  const int w_dtype = require_weights(weights, rows, device);
+  const int64_t h = y.size(1);
+  const c10::DeviceGuard guard(device);
+  Tensor dy, dw;
+  if (row_grad) dy = empty(y.sizes(), y.scalar_type(), device);
+  if (weight_grad) dw = empty(rows.sizes(), scalar_type(w_dtype), device);
+  check_status(fp8bsq_expert_combine_backward(dout.data_ptr(), y.data_ptr(), dtype, c.rows, data_or_null(weights),
+                                              w_dtype, c.tokens, c.top_k, h, row_grad ? dy.data_ptr() : nullptr,
+                                              weight_grad ? dw.data_ptr() : nullptr, stream_of(device)));
+  return py::make_tuple(or_none(dy), or_none(dw));
+}
+
+// [E, F, K] codes and their scales; f, k and experts from the first.
+Weight expert_weight(const Tensor &w, const Tensor &s, at::IntArrayRef shape) {
+  if (w.dim() != 3 || w.sizes() != shape) value("weights must be [E, F, K] with a's K, all of one shape");
+  if (s.scalar_type() != at::kFloat) type("scales must be float32");
+  if (s.dim() != 3 || s.size(0) != shape[0] || s.size(1) != (shape[1] + 127) / 128 || s.size(2) != shape[2] / 128)
+    value("the weights' scales must be [E, ceil(F/128), K/128]");
+  return {(const uint8_t *)w.data_ptr(), (const float *)s.data_ptr()};
+}
+
+// The product with one weight (w1 null), or the gated one.
+Tensor expert_product(const Tensor &a, const Tensor &a_s, const Tensor &offsets, const Tensor &w0, const Tensor &w0_s,
+                      const Tensor *w1, const Tensor *w1_s, int out_dtype) {
+  for (const Tensor *t : {&a, &w0}) require_codes(*t);
+  if (w1) require_codes(*w1);
+  const c10::Device device = a.device();
+  for (const Tensor *t : {&a, &a_s, &offsets, &w0, &w0_s}) require_gpu(*t, device);
+  if (w1)
+    for (const Tensor *t : {w1, w1_s}) require_gpu(*t, device);
+  if (a.dim() != 2 || a.size(1) <= 0 || a.size(1) % 128 != 0) value("a must be [R, K], K a positive multiple of 128");
+  const int64_t rows = a.size(0), k = a.size(1);
+  if (a_s.scalar_type() != at::kFloat) type("scales must be float32");
+  if (a_s.dim() != 2 || a_s.size(0) != rows || a_s.size(1) != k / 128) value("a_s must be [R, K/128]");
+  if (w0.dim() != 3 || w0.size(0) <= 0 || w0.size(2) != k) value("weights must be [E, F, K] with a's K, all of one shape");
+  const int64_t experts = w0.size(0), f = w0.size(1);
+  const Weight first = expert_weight(w0, w0_s, w0.sizes());
+  const Weight second = w1 ? expert_weight(*w1, *w1_s, w0.sizes()) : Weight{nullptr, nullptr};
+  if (offsets.scalar_type() != at::kInt) type("offsets must be int32, as expert_sort returns them");
+  if (offsets.dim() != 1 || offsets.size(0) != experts + 1) value("offsets must be [E + 1]");
+  const c10::DeviceGuard guard(device);
+  const Tensor out = empty({rows, f}, scalar_type(out_dtype), device);
+  const uint8_t *codes = (const uint8_t *)a.data_ptr();
+  const float *scales = (const float *)a_s.data_ptr();
+  const int32_t *begin = (const int32_t *)offsets.data_ptr();
+  check_status(w1 ? fp8_expert_gated_ffn(codes, scales, begin, first.codes, first.scales, second.codes, second.scales,
+                                         out.data_ptr(), out_dtype, rows, experts, f, k, stream_of(device))
+                  : fp8_expert_gemm(codes, scales, begin, first.codes, first.scales, out.data_ptr(), out_dtype, rows,
+                                    experts, f, k, stream_of(device)));
+  return out;
+}
+
+Tensor expert_gemm(const Tensor &a, const Tensor &a_s, const Tensor &offsets, const Tensor &b, const Tensor &b_s,
+                   int out_dtype) {
+  return expert_product(a, a_s, offsets, b, b_s, nullptr, nullptr, out_dtype);
+}
+
+Tensor expert_gated_ffn(const Tensor &a, const Tensor &a_s, const Tensor &offsets, const Tensor &w_gate,
+                        const Tensor &w_gate_s, const Tensor &w_up, const Tensor &w_up_s, int out_dtype) {
+  return expert_product(a, a_s, offsets, w_gate, w_gate_s, &w_up, &w_up_s, out_dtype);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_ffn_ext, m) {
@@ -242,4 +417,11 @@ PYBIND11_MODULE(_ffn_ext, m) {
   m.def("fp4_weight_quant", &fp4_quantize);
   m.def("fp4_gemv", &fp4_product);
   m.def("clip_grad_norm", &clip);
+  m.def("expert_sort", &expert_sort);
+  m.def("expert_dispatch", &expert_dispatch);
+  m.def("expert_dispatch_quant", &expert_dispatch_quant);
+  m.def("expert_combine", &expert_combine);
+  m.def("expert_combine_backward", &expert_combine_backward);
+  m.def("expert_gemm", &expert_gemm);
+  m.def("expert_gated_ffn", &expert_gated_ffn);
 }

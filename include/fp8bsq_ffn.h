@@ -2,8 +2,9 @@
  * fp8bsq_ffn.h -- C ABI of the feed-forward operators on the block-scaled
  * formats of fp8bsq.h, for AMD Instinct MI355X (gfx950): the gated
  * feed-forward block and its backward pass, 4-bit weights with the
- * matrix-vector product that reads them, and gradient clipping by the global
- * norm.  They live in libfp8bsq_ffn.so, which uses libfp8bsq.so.
+ * matrix-vector product that reads them, gradient clipping by the global norm,
+ * and the same block behind a router: tokens sorted by expert and back, and the
+ * experts' products.  They live in libfp8bsq_ffn.so, which uses libfp8bsq.so.
  *
  * The conventions of fp8bsq.h hold here too: device pointers owned by the
  * caller, dense row-major tensors, work queued on `hip_stream` without
@@ -155,6 +156,120 @@ FP8BSQ_API int fp8bsq_clip_grad_norm(const void *const *grads, void *const *outs
                           const int32_t *dtypes, int64_t count, float max_norm, float eps, float *norm,
                           void *workspace, size_t workspace_bytes, void *hip_stream);
 FP8BSQ_API size_t fp8bsq_clip_grad_norm_workspace(int64_t count);
+
+/*
+ * The expert operators.  `tokens` tokens choose `top_k` experts each; choice
+ * c = t * top_k + j is token t's j-th.  The n = tokens * top_k choices, sorted by
+ * expert, have a row each:
+ *
+ *   offsets  [num_experts + 1] int32: expert e's rows are offsets[e] .. offsets[e + 1] - 1.
+ *   rows     [n] int32: choice c's row r; ~r (negative) for a choice that takes no
+ *            part, its row then being one of those behind, from offsets[num_experts] on.
+ *
+ * Sizes: tokens >= 0, top_k >= 1, n < 2^31, 1 <= num_experts <= 1024, and the
+ * rows' lengths as the entry points say; else FP8BSQ_ERANGE (negative sizes,
+ * top_k = 0 and num_experts = 0: FP8BSQ_EINVAL).  What offsets and rows hold is not
+ * checked; other contents than fp8bsq_expert_sort's give unspecified but
+ * memory-safe outputs.
+ */
+
+/*
+ * fp8bsq_expert_sort -- the stable sort of the choices by expert.
+ *
+ *   experts  [n] expert numbers, int32 or int64 (index_bytes 4 or 8), aligned to
+ *            their size.  A number outside 0 .. num_experts - 1 takes no part: a
+ *            padded token's, or an expert's of another rank.
+ *   offsets, rows, choices   out, 4-byte aligned: the above, and [n] int32 the
+ *            choice of each row (the inverse of rows, also behind).
+ *            Within an expert, and behind, rows follow the order of the choices.
+ *   n = 0    offsets are set to zero.
+ *   workspace   may be NULL where its size is 0.
+ */
+FP8BSQ_API int fp8bsq_expert_sort(const void *experts, int index_bytes, int64_t n, int64_t num_experts, int32_t *offsets,
+                       int32_t *rows, int32_t *choices, void *workspace, size_t workspace_bytes, void *hip_stream);
+FP8BSQ_API size_t fp8bsq_expert_sort_workspace(int64_t n, int64_t num_experts);
+
+/*
+ * fp8bsq_expert_dispatch -- y[rows[c]] = x[c / top_k], and zeros in the rows behind.
+ *
+ *   x        [tokens, h], y [n, h] out, both of `dtype`, aligned to their elements.
+ *   h        0 <= h <= 2^21.
+ *
+ * Its gradient is fp8bsq_expert_combine with weights NULL.
+ */
+FP8BSQ_API int fp8bsq_expert_dispatch(const void *x, int dtype, const int32_t *rows, int64_t tokens, int64_t top_k, int64_t h,
+                           void *y, void *hip_stream);
+
+/*
+ * fp8_expert_dispatch_quant -- fp8_act_quant of that, each token quantized once.
+ *
+ *   x        [tokens, h], dtype x_dtype, 16-byte aligned; h % 128 == 0 (else
+ *            FP8BSQ_ESHAPE).
+ *   y, s     [n, h] E4M3 codes out, 16-byte aligned, and [n, h / 128] FP32 scales
+ *            out, 4-byte aligned; the rows behind are those of rows of zeros.
+ */
+FP8BSQ_API int fp8_expert_dispatch_quant(const void *x, int x_dtype, int scale_fmt, const int32_t *rows, int64_t tokens,
+                              int64_t top_k, int64_t h, uint8_t *y, float *s, void *hip_stream);
+
+/*
+ * fp8bsq_expert_combine -- out[t] = sum over j of weights[t, j] y[rows[t, j]], in
+ * FP32 and j's order; choices that take no part are left out, and what y holds in
+ * the rows behind is not read.
+ *
+ *   y        [n, h], out [tokens, h] out, both of `dtype`, aligned to their
+ *            elements.  No other tensor overlaps out.
+ *   weights  [tokens, top_k], dtype w_dtype, aligned to its elements, or NULL: ones.
+ *   h        0 <= h <= 2^21.
+ */
+FP8BSQ_API int fp8bsq_expert_combine(const void *y, int dtype, const int32_t *rows, const void *weights, int w_dtype,
+                          int64_t tokens, int64_t top_k, int64_t h, void *out, void *hip_stream);
+
+/*
+ * fp8bsq_expert_combine_backward --
+ *     dy[rows[t, j]] = weights[t, j] dout[t]             (rows behind: zero)
+ *     dweights[t, j] = sum of dout[t] * y[rows[t, j]]    (taking no part: zero)
+ *
+ *   dout     [tokens, h], y [n, h], dy [n, h] out, of `dtype`.
+ *   dy       or NULL: not computed.
+ *   dweights [tokens, top_k] out, dtype w_dtype, or NULL: not computed (y is not
+ *            read and may then be NULL).  Sums are FP32, in a fixed order.
+ */
+FP8BSQ_API int fp8bsq_expert_combine_backward(const void *dout, const void *y, int dtype, const int32_t *rows,
+                                   const void *weights, int w_dtype, int64_t tokens, int64_t top_k, int64_t h, void *dy,
+                                   void *dweights, void *hip_stream);
+
+/*
+ * fp8_expert_gemm -- c[r] = a[r] . b[e]^T for expert e's rows r, fp8_block_gemm's
+ * product; the rows behind are zero.
+ *
+ *   a, a_s   [rows, k] E4M3 codes, 16-byte aligned, and [rows, k / 128] FP32
+ *            scales, 4-byte aligned; the rows behind are not read.
+ *   offsets  as fp8bsq_expert_sort writes them.
+ *   b, b_s   [num_experts, n, k] E4M3 codes, 16-byte aligned, and
+ *            [num_experts, ceil(n / 128), k / 128] FP32 scales, 4-byte aligned.
+ *   c        [rows, n] out, dtype c_dtype, aligned to its elements.
+ *   sizes    rows, n >= 0; k >= 128, k % 128 == 0 (else FP8BSQ_ESHAPE; k = 0 is
+ *            FP8BSQ_EINVAL); rows <= 65535 * 16, n, k <= 2^21, num_experts as above
+ *            (else FP8BSQ_ERANGE).  rows or n = 0: nothing to do.
+ *
+ * Results meet fp8_block_gemm's error bound.
+ */
+FP8BSQ_API int fp8_expert_gemm(const uint8_t *a, const float *a_s, const int32_t *offsets, const uint8_t *b,
+                    const float *b_s, void *c, int c_dtype, int64_t rows, int64_t num_experts, int64_t n, int64_t k,
+                    void *hip_stream);
+
+/*
+ * fp8_expert_gated_ffn -- h[r] = silu(g) * u, g = a[r] . w_gate[e]^T and
+ * u = a[r] . w_up[e]^T: fp8_gated_ffn of each expert's rows, already quantized.
+ *
+ *   w_gate, w_up, .._s   [num_experts, f, k] and [num_experts, ceil(f / 128), k / 128].
+ *   h        [rows, f] out, dtype out_dtype, aligned to its elements; the rows
+ *            behind are zero.
+ *   others, sizes        as for fp8_expert_gemm.
+ */
+FP8BSQ_API int fp8_expert_gated_ffn(const uint8_t *a, const float *a_s, const int32_t *offsets, const uint8_t *w_gate,
+                         const float *w_gate_s, const uint8_t *w_up, const float *w_up_s, void *h, int out_dtype,
+                         int64_t rows, int64_t num_experts, int64_t f, int64_t k, void *hip_stream);
 
 #ifdef __cplusplus
 }
