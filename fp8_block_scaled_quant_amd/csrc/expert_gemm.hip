@@ -2,6 +2,16 @@
 // gfx950: out[r] = a[r] W[e]^T for offsets[e] <= r < offsets[e + 1], or with two
 // weights silu(a[r] Wg[e]^T) * (a[r] Wu[e]^T).  Each 128-wide K block's partial is
 // multiplied by a_s[r, kb] * w_s[e, j / 128, kb] and added in FP32.
+//
+// How many rows an expert has is known on the device alone.  Every workgroup reads
+// the offsets, works out the tiles of all experts, and takes its share of them;
+// the launch depends on sizes only.  Within an expert the tiles of one piece of
+// weight follow each other, so that it comes from HBM once.
+//
+// Two kernels: tiles of up to 128 rows by 128 rows of weights, with transfers many
+// blocks ahead, for few rows an expert (bound by the weights' bytes), and of 256 by
+// 256, for many (bound by the matrix cores).
+#include "device_cus.h"
 #include "e4m3_tiles.h"
 #include "expert_launch.h"
 
@@ -17,52 +27,579 @@ struct ProductArgs {
   void *out;
   int64_t rows, f, k;
   int experts, nkb;
-  bool out_bf16;
+  int tiles_f, blocks_f;    // tiles and 128-wide blocks of the features
+  bool out_bf16, vec;
 };
 
-// A wave per 16 features; a workgroup's four waves go through the expert's rows
-// 16 at a time.  The last expert's workgroups clear the rows behind.
-template <bool kGated>
-__global__ __launch_bounds__(256) void product_simple_kernel(const ProductArgs p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, fq = lane >> 4;
-  const int e = blockIdx.y;
-  const int64_t f0 = ((int64_t)blockIdx.x * 4 + wave) * 16;
-  if (f0 >= p.f) return;
-  const int64_t feature = min(f0 + fr, p.f - 1);
-  const int64_t begin = min(max((int64_t)p.offsets[e], (int64_t)0), p.rows);
-  const int64_t end = min(max((int64_t)p.offsets[e + 1], begin), p.rows);
-  const int64_t grid_rows = (p.f + kBlock - 1) / kBlock;
-  const float *s0 = p.w0_s + ((int64_t)e * grid_rows + f0 / kBlock) * p.nkb;
-  const float *s1 = kGated ? p.w1_s + ((int64_t)e * grid_rows + f0 / kBlock) * p.nkb : nullptr;
-  for (int64_t r0 = begin; r0 < end; r0 += 16) {
-    const int64_t row = min(r0 + fr, end - 1);
-    f32x4 g = {0.f, 0.f, 0.f, 0.f}, u = g;
-    for (int kb = 0; kb < p.nkb; ++kb) {
-      const i32x8 a = load_frag(p.a + row * p.k + kb * kBlock + 32 * fq);
-      const float sa = p.a_s[row * p.nkb + kb];
-      const int64_t at = ((int64_t)e * p.f + feature) * p.k + kb * kBlock + 32 * fq;
-      const f32x4 v0 = mfma_e4m3_16x16x128(load_frag(p.w0 + at), a, f32x4{0.f, 0.f, 0.f, 0.f});
+// The experts' rows as the offsets give them, in order and inside the matrix
+// whatever the offsets hold, and their token tiles' numbers.
+struct Table {
+  int begin[kMaxExperts + 1];   // expert's first row; the last: where the rows behind begin
+  int first[kMaxExperts + 1];   // its first token tile; the last: their number
+};
+
+__device__ __forceinline__ int wave_max_scan(int v, int lane) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) g[i] = __builtin_fmaf(v0[i], sa * s0[kb], g[i]);
-      if (kGated) {
-        const f32x4 v1 = mfma_e4m3_16x16x128(load_frag(p.w1 + at), a, f32x4{0.f, 0.f, 0.f, 0.f});
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v = max(v, o);
+  }
+  return v;
+}
+
+__device__ __forceinline__ int wave_sum_scan(int v, int lane) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = __builtin_fmaf(v1[i], sa * s1[kb], u[i]);
-      }
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// By all kThreads threads, kThreads experts at a time.
+template <int kThreads, int kTokens>
+__device__ __forceinline__ void build_table(const ProductArgs &p, Table &t) {
+  __shared__ int top[kThreads / 64], sum[kThreads / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto inside = [&](int v) { return min(max(v, 0), (int)p.rows); };
+  int rows_before = inside(p.offsets[0]), tiles_before = 0;
+  for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
+    const int e = e0 + threadIdx.x;
+    const int m = wave_max_scan(e < p.experts ? inside(p.offsets[e + 1]) : 0, lane);
+    if (lane == 63) top[wave] = m;
+    __syncthreads();
+    int before = rows_before;
+    for (int w = 0; w < kThreads / 64; ++w) {
+      if (w < wave) before = max(before, top[w]);
+      rows_before = max(rows_before, top[w]);
     }
-    if (r0 + fr < end) {
+    const int prev = __shfl_up(m, 1), begin = lane ? max(prev, before) : before, end = max(m, before);
+    const int tiles = (end - begin + kTokens - 1) / kTokens;
+    const int s = wave_sum_scan(tiles, lane);
+    if (lane == 63) sum[wave] = s;
+    __syncthreads();
+    int at = tiles_before;
+    for (int w = 0; w < kThreads / 64; ++w) {
+      if (w < wave) at += sum[w];
+      tiles_before += sum[w];
+    }
+    if (e < p.experts) {
+      t.begin[e] = begin;
+      t.first[e] = at + s - tiles;
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    t.begin[p.experts] = rows_before;
+    t.first[p.experts] = tiles_before;
+  }
+  __syncthreads();
+}
+
+// A tile: `left` rows from row0, and the features from f0 (clipped at f).
+struct Tile {
+  int expert, row0, left;
+  int64_t f0;
+};
+
+// Tile of turn `it`: workgroups are dealt round-robin to the eight XCDs, so turns
+// it, it + 8, ... get consecutive tiles of one XCD's contiguous share (they then
+// share its L2).  The same in every lane.
+template <int kTokens, int kFeatures>
+__device__ __forceinline__ Tile locate(const ProductArgs &p, const Table &t, uint32_t it, uint32_t ntiles, int lane) {
+  const uint32_t base = ntiles / 8, rest = ntiles % 8, xcd = it % 8;
+  const uint32_t tile = xcd * base + min(xcd, rest) + it / 8, q = tile / (uint32_t)p.tiles_f;
+  int e = 0;   // experts whose tiles end at or before token tile q
+  for (int e0 = 1; e0 <= p.experts; e0 += 64) {
+    const bool ended = e0 + lane <= p.experts && (uint32_t)t.first[min(e0 + lane, p.experts)] <= q;
+    e += __popcll(__ballot(ended));
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int first = __builtin_amdgcn_readfirstlane(t.first[e]), tokens = __builtin_amdgcn_readfirstlane(t.first[e + 1]) - first;
+  const uint32_t rem = tile - (uint32_t)first * p.tiles_f;
+  const int tf = rem / tokens, ta = rem - (uint32_t)tf * tokens;
+  Tile r;
+  r.expert = e;
+  r.row0 = __builtin_amdgcn_readfirstlane(t.begin[e]) + ta * kTokens;
+  r.left = min(__builtin_amdgcn_readfirstlane(t.begin[e + 1]) - r.row0, kTokens);
+  r.f0 = (int64_t)tf * kFeatures;
+  return r;
+}
+
+// Zeros in the rows behind the experts', by all workgroups' `threads` first threads.
+__device__ __forceinline__ void clear_behind(const ProductArgs &p, int behind, int threads) {
+  const int64_t size = p.out_bf16 ? 2 : 4;
+  uint8_t *begin = (uint8_t *)p.out + behind * p.f * size, *end = (uint8_t *)p.out + p.rows * p.f * size;
+  const int64_t self = (int64_t)blockIdx.x * threads + threadIdx.x, all = (int64_t)gridDim.x * threads;
+  uint8_t *inner = (uint8_t *)(((uintptr_t)begin + 15) & ~(uintptr_t)15), *inner_end = (uint8_t *)((uintptr_t)end & ~(uintptr_t)15);
+  if (inner >= inner_end) {   // a few elements
+    for (int64_t i = self; i < (end - begin) / 2; i += all) ((uint16_t *)begin)[i] = 0;
+    return;
+  }
+  for (int64_t i = self; i < (inner_end - inner) / 16; i += all) ((u32x4 *)inner)[i] = u32x4{0, 0, 0, 0};
+  for (int64_t i = self; i < (inner - begin) / 2; i += all) ((uint16_t *)begin)[i] = 0;
+  for (int64_t i = self; i < (end - inner_end) / 2; i += all) ((uint16_t *)inner_end)[i] = 0;
+}
+
+// Four consecutive outputs of a row.
+__device__ __forceinline__ void store_four(const ProductArgs &p, int64_t row, int64_t col, f32x4 v) {
+  const int64_t at = row * p.f + col;
+  const int left = (int)min((int64_t)4, p.f - col);
+  if (p.out_bf16) {
+    if (p.vec) store4<true, true>(p.out, at, v, 4); else store4<true, false>(p.out, at, v, left);
+  } else {
+    if (p.vec) store4<false, true>(p.out, at, v, 4); else store4<false, false>(p.out, at, v, left);
+  }
+}
+
+__device__ __forceinline__ f32x4 gated4(f32x4 g, f32x4 u) {
+  f32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = gated(g[i], u[i]);
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows an expert: kTokens rows by 128 rows of weights.
+//
+// Four compute waves, and movers that issue all global->LDS transfers into a ring
+// of kSlots blocks of 128, kSlots - 1 ahead, over the ends of tiles: a workgroup's
+// blocks are one sequence.  That keeps enough bytes in flight to stream weights
+// (16 KB a block) at HBM's rate, also where tiles are short.  One barrier a block
+// hands the ring on; a block's fragments are read to registers while the block
+// before it feeds the MFMAs.
+// ---------------------------------------------------------------------------
+constexpr int kStreamRows = 128;   // of weights, a tile
+
+template <int kTokens>
+struct StreamShape {
+  static constexpr int kSlots = kTokens == 128 ? 4 : kTokens == 64 ? 5 : 7;
+  static constexpr int kMovers = kTokens == 128 ? 1 : kTokens == 64 ? 2 : 4;   // of weights; one more of a
+  static constexpr int kThreads = 64 * (4 + kMovers + 1);
+  static constexpr int kAcross = kTokens >= 64 ? 2 : 4;    // compute waves along the weights' rows
+  static constexpr int kI = kTokens / 16 / (4 / kAcross);  // MFMA tiles of a wave along the tokens,
+  static constexpr int kJ = kStreamRows / 16 / kAcross;    // and along the weights
+  static constexpr int kScales = kTokens < 64 ? 64 : kTokens;
+  static constexpr int kSlotBytes = (kTokens + kStreamRows) * kBlock + kScales * 4;
+  static constexpr int kDmaA = kTokens / 8 + kScales / 64, kDmaB = 16 / kMovers;   // transfers a block and mover
+  static_assert((kSlots - 1) * (kDmaA > kDmaB ? kDmaA : kDmaB) < 64, "the wait counter's range");
+};
+
+template <bool kGated, int kTokens>
+__global__ __launch_bounds__(StreamShape<kTokens>::kThreads) void product_stream_kernel(const ProductArgs p) {
+  using S = StreamShape<kTokens>;
+  constexpr int kFeatures = kGated ? kStreamRows / 2 : kStreamRows;
+  constexpr int kWaveRows = kStreamRows / S::kAcross;   // of weights, a compute wave; gated: gate's, then up's
+  constexpr int kAhead = S::kSlots - 1;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[S::kSlots * S::kSlotBytes];
+  __shared__ Table table;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fr = lane & 15, fq = lane >> 4, dr = lane >> 3, ds = lane & 7;
+  build_table<S::kThreads, kTokens>(p, table);
+  const uint32_t ntiles = (uint32_t)__builtin_amdgcn_readfirstlane(table.first[p.experts]) * (uint32_t)p.tiles_f;
+  const int nkb = p.nkb;
+  const uint32_t mine = blockIdx.x < ntiles ? (ntiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+  const int64_t blocks = (int64_t)mine * nkb;
+  auto tile_of = [&](uint32_t i) { return locate<kTokens, kFeatures>(p, table, blockIdx.x + i * gridDim.x, ntiles, lane); };
+
+  if (wave >= 4) {
+    // Movers: the first of a and its scales, the others of the weights.  Past the
+    // end they issue the last block again, so that every block counts the same.
+    if (blocks == 0) return;
+    uint32_t turn = 0;
+    int kb = 0, slot = 0;
+    auto drive = [&](auto enter, auto issue, auto wait_landed) __attribute__((always_inline)) {
+#pragma unroll 1
+      for (int64_t s = 0; s < blocks + kAhead; ++s) {
+        if (kb == 0) enter(tile_of(turn));
+        issue((int64_t)kb, lds_addr(ring) + (uint32_t)slot * S::kSlotBytes);   // into the slot of block s - kSlots, whose reads ended before the last barrier
+        slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+        if (kb + 1 < nkb) {
+          ++kb;
+        } else if (turn + 1 < mine) {
+          ++turn;
+          kb = 0;
+        }
+        if (s >= kAhead - 1) {
+          wait_landed();   // all but the youngest kAhead - 1 blocks
+          workgroup_barrier();
+        }
+      }
+      wait_dma_all();   // transfers past the end, before the workgroup's LDS is released
+    };
+    // lane p of an 8-row group fills chunk slot p % 8 of row p / 8; rows past an
+    // edge re-read the last one
+    if (wave == 4) {
+      uint32_t off[kTokens / 8], s_off[S::kScales / 64];
+      const uint8_t *base = nullptr;
+      const float *scales = nullptr;
+      drive(
+          [&](const Tile &t) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kTokens / 8; ++i) {
+              const int row = 8 * i + dr;
+              off[i] = (uint32_t)min(row, t.left - 1) * (uint32_t)p.k + ((ds ^ swz(row)) << 4);
+            }
+#pragma unroll
+            for (int i = 0; i < S::kScales / 64; ++i) s_off[i] = (uint32_t)min(64 * i + lane, t.left - 1) * (uint32_t)nkb * 4;
+            base = p.a + (int64_t)t.row0 * p.k;
+            scales = p.a_s + (int64_t)t.row0 * nkb;
+          },
+          [&](int64_t kb, uint32_t to) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kTokens / 8; ++i) lds_dma16(base + kb * kBlock, off[i], to + i * 1024);
+#pragma unroll
+            for (int i = 0; i < S::kScales / 64; ++i)
+              lds_dma4(scales + kb, s_off[i], to + (kTokens + kStreamRows) * kBlock + i * 256);
+          },
+          [&]() __attribute__((always_inline)) { asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * S::kDmaA) : "memory"); });
+    } else {
+      const int group0 = (wave - 5) * S::kDmaB;   // of the weights' 16 groups of 8 rows
+      uint32_t off[S::kDmaB];
+      const uint8_t *base0 = nullptr, *base1 = nullptr;
+      drive(
+          [&](const Tile &t) __attribute__((always_inline)) {
+            const int left = (int)min((int64_t)kFeatures, p.f - t.f0);
+#pragma unroll
+            for (int i = 0; i < S::kDmaB; ++i) {
+              const int row = 8 * (group0 + i) + dr;
+              const int feature = kGated ? row / kWaveRows * (kWaveRows / 2) + row % (kWaveRows / 2) : row;
+              off[i] = (uint32_t)min(feature, left - 1) * (uint32_t)p.k + ((ds ^ swz(row)) << 4);
+            }
+            const int64_t at = ((int64_t)t.expert * p.f + t.f0) * p.k;
+            base0 = p.w0 + at;
+            base1 = kGated ? p.w1 + at : base0;
+          },
+          [&](int64_t kb, uint32_t to) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < S::kDmaB; ++i) {
+              const bool up = kGated && (8 * (group0 + i) / (kWaveRows / 2) & 1);
+              lds_dma16((up ? base1 : base0) + kb * kBlock, off[i], to + kTokens * kBlock + (group0 + i) * 1024);
+            }
+          },
+          [&]() __attribute__((always_inline)) { asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * S::kDmaB) : "memory"); });
+    }
+    return;
+  }
+
+  const int wa = wave / S::kAcross * (S::kI * 16), wb = wave % S::kAcross;
+  if (blocks > 0) {
+    struct Block {
+      i32x8 a[S::kI], b[S::kJ];
+      float sa[S::kI], w[2];
+    };
+    f32x4 acc[S::kI][S::kJ];   // gated: row tiles gate's, then up's
+    auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < S::kI; ++i)
+#pragma unroll
+        for (int j = 0; j < S::kJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+    // the block read next, and the tile being computed
+    uint32_t turn = 0;
+    int kb = 0, slot = 0, done = 0;
+    Tile ahead = tile_of(0), tile = ahead;
+    auto read = [&](Block &v) __attribute__((always_inline)) {
+      const uint8_t *a = ring + slot * S::kSlotBytes, *b = a + kTokens * kBlock;
+      const float *as = (const float *)(b + kStreamRows * kBlock);
+      const int64_t at = ((int64_t)ahead.expert * p.blocks_f + ahead.f0 / kBlock) * nkb + kb;
+      v.w[0] = load_uniform(p.w0_s, at);
+      if (kGated) v.w[1] = load_uniform(p.w1_s, at);
+#pragma unroll
+      for (int j = 0; j < S::kJ; ++j) {
+        const int r = kWaveRows * wb + 16 * j + fr;
+        v.b[j] = frag_from_lds(b + r * kBlock, fq, r);
+      }
+#pragma unroll
+      for (int i = 0; i < S::kI; ++i) {
+        const int r = wa + 16 * i + fr;
+        v.a[i] = frag_from_lds(a + r * kBlock, fq, r);
+        v.sa[i] = as[r];
+      }
+      slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+      if (kb + 1 < nkb) {
+        ++kb;
+      } else if (turn + 1 < mine) {
+        ++turn;
+        kb = 0;
+        ahead = tile_of(turn);
+      }
+    };
+    auto compute = [&](const Block &v) __attribute__((always_inline)) {
+      // the rescale of an MFMA's partial runs behind the next ones
+      constexpr int kN = S::kI * S::kJ, kBehind = kN < 4 ? kN - 1 : 3;
+      f32x4 prt[kBehind + 1];
+      auto rescale = [&](int q) {
+        const int i = q % S::kI, j = q / S::kI;
+        const float sc = v.sa[i] * v.w[kGated && j >= S::kJ / 2 ? 1 : 0];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(prt[q % (kBehind + 1)][e], sc, acc[i][j][e]);
+      };
+#pragma unroll
+      for (int q = 0; q < kN; ++q) {
+        prt[q % (kBehind + 1)] = mfma_e4m3_16x16x128(v.b[q / S::kI], v.a[q % S::kI], f32x4{0.f, 0.f, 0.f, 0.f});
+        if (q >= kBehind) rescale(q - kBehind);
+      }
+#pragma unroll
+      for (int q = kN - kBehind; q < kN; ++q) rescale(q);
+    };
+    auto finish = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < S::kI; ++i) {
+        const int r = wa + 16 * i + fr;
+        if (r >= tile.left) continue;
+#pragma unroll
+        for (int j = 0; j < (kGated ? S::kJ / 2 : S::kJ); ++j) {
+          const int64_t col = tile.f0 + (kGated ? kWaveRows / 2 : kWaveRows) * wb + 16 * j + 4 * fq;
+          if (col < p.f)
+            store_four(p, tile.row0 + r, col, kGated ? gated4(acc[i][j], acc[i][j + S::kJ / 2]) : acc[i][j]);
+        }
+      }
+    };
+    Block even, odd;
+    workgroup_barrier();
+    clear();
+    read(even);
+    auto step = [&](int64_t s, const Block &cur, Block &next) __attribute__((always_inline)) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // block s's reads ended: its slot may be refilled
+      workgroup_barrier();                                 // s + 1 landed
+      const Tile then = ahead;
+      if (s + 1 < blocks) read(next);
+      __builtin_amdgcn_sched_barrier(0);
+      if (wa < tile.left) compute(cur);
+      __builtin_amdgcn_sched_barrier(0);
+      if (++done == nkb) {
+        finish();
+        clear();
+        done = 0;
+        tile = then;   // the next block's
+      }
+    };
+    int64_t s = 0;
+#pragma nounroll
+    for (; s + 1 < blocks; s += 2) {
+      step(s, even, odd);
+      step(s + 1, odd, even);
+    }
+    if (s < blocks) step(s, even, odd);
+  }
+  clear_behind(p, table.begin[p.experts], 256);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows an expert: 256 rows by 256 rows of weights (gated: 128 features' gate
+// and up).
+//
+// Workgroup: 512 threads = 8 waves, 4 x 2, a wave 64 rows by 128 rows of weights
+// (4 x 8 MFMA tiles, two waves per SIMD); gated, in each half 64 gate rows and the
+// 64 up rows of the same features.  A two-stage LDS ring by direct global->LDS
+// transfers, block kb + 1 loaded while kb is computed, over the ends of tiles.
+// The rescale of an MFMA's partial runs three MFMAs behind it.  Waves whose rows an
+// expert does not have skip their MFMAs: a tile of up to 128 rows keeps one wave a
+// SIMD.
+// ---------------------------------------------------------------------------
+template <bool kGated>
+__global__ __launch_bounds__(kBigThreads) void product_big_kernel(const ProductArgs p) {
+  constexpr int kFeatures = kGated ? kBigTile / 2 : kBigTile;
+  struct Smem {
+    uint8_t a[2][kBigTile * kBlock];
+    uint8_t b[2][kBigTile * kBlock];
+    float as[2][kBigTile];
+  };
+  __shared__ __attribute__((aligned(1024))) Smem sm;
+  __shared__ Table table;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nkb = p.nkb;
+  const int wa = (wave >> 1) * 64, wb = wave & 1;   // wave's rows, and half of the weights' rows
+  const int fr = lane & 15, fq = lane >> 4;
+  // transfers: lane p of an 8-row group fills chunk slot p % 8 of row p / 8; a's
+  // group 8 d + g by wave d < 4, the weights' group 4 w + i by every wave w
+  const bool dma_wave = wave < 4;
+  const int dw = wave & 3, dr = lane >> 3, ds = lane & 7;
+  const uint32_t lds_a = lds_addr(&sm.a[0][0]), lds_b = lds_addr(&sm.b[0][0]), lds_as = lds_addr(&sm.as[0][0]);
+  build_table<kBigThreads, kBigTile>(p, table);
+  const uint32_t ntiles = (uint32_t)__builtin_amdgcn_readfirstlane(table.first[p.experts]) * (uint32_t)p.tiles_f;
+
+  uint32_t a_off[8], b_off[4], s_off = 0;   // from the tile's own base
+  const uint8_t *a_base = nullptr, *b_base = nullptr;
+  const float *as_base = nullptr;
+  auto set_offsets = [&](const Tile &t) {   // rows past an edge re-read the last one
+    a_base = p.a + (int64_t)t.row0 * p.k;
+    as_base = p.a_s + (int64_t)t.row0 * nkb;
+    s_off = (uint32_t)min(64 * dw + lane, t.left - 1) * (uint32_t)nkb * 4;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const int row = 8 * (8 * dw + g) + dr;
+      a_off[g] = (uint32_t)min(row, t.left - 1) * (uint32_t)p.k + ((ds ^ swz(row)) << 4);
+    }
+    b_base = (kGated && (wave & 2) ? p.w1 : p.w0) + ((int64_t)t.expert * p.f + t.f0) * p.k;
+    const int left = (int)min((int64_t)kFeatures, p.f - t.f0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 8 * (4 * wave + i) + dr;   // gated: half row / 128, projection (row / 64) % 2
+      const int r = kGated ? (row >> 7) * 64 + (row & 63) : row;
+      b_off[i] = (uint32_t)min(r, left - 1) * (uint32_t)p.k + ((ds ^ swz(row)) << 4);
+    }
+  };
+  auto issue_a = [&](int kb, int s) {
+    const uint8_t *ab = a_base + (int64_t)kb * kBlock;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) lds_dma16(ab, a_off[g], lds_a + s * (kBigTile * kBlock) + (8 * dw + g) * 1024);
+    lds_dma4(as_base + kb, s_off, lds_as + s * (kBigTile * 4) + dw * 256);
+  };
+  auto issue_b = [&](int kb, int s) {
+    const uint8_t *bb = b_base + (int64_t)kb * kBlock;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lds_dma16(bb, b_off[i], lds_b + s * (kBigTile * kBlock) + (4 * wave + i) * 1024);
+  };
+
+  int stage = 0;
+  bool landed = false;
+  Tile tile;
+  if (blockIdx.x < ntiles) {
+    tile = locate<kBigTile, kFeatures>(p, table, blockIdx.x, ntiles, lane);
+    set_offsets(tile);
+    if (dma_wave) issue_a(0, 0);
+    issue_b(0, 0);
+  }
+  for (uint32_t it = blockIdx.x; it < ntiles; it += gridDim.x) {
+    const bool more = it + gridDim.x < ntiles;
+    Tile next = tile;
+    if (more) next = locate<kBigTile, kFeatures>(p, table, it + gridDim.x, ntiles, lane);
+    const bool live = wa < tile.left;
+    // the wave's features lie in one block column
+    const int64_t wcol = min(tile.f0 / kBlock + (kGated ? 0 : wb), (int64_t)p.blocks_f - 1);
+    const int64_t w_at = ((int64_t)tile.expert * p.blocks_f + wcol) * nkb;
+
+    f32x4 acc[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 prt[4];
+    float sc[2][4];   // row scale * weight scale, per projection
+#pragma unroll
+    for (int q = 0; q < 4; ++q) prt[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[0][i] = sc[1][i] = 0.f;
+    auto rescale = [&](int qp) {   // MFMA qp = 4 j + i
+      const int ip = qp % 4, jp = qp / 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[ip][jp][e] = __builtin_fmaf(prt[qp % 4][e], sc[kGated ? jp / 4 : 0][ip], acc[ip][jp][e]);
+    };
+
+#pragma nounroll
+    for (int kb = 0; kb < nkb; ++kb, stage ^= 1) {
+      const int cur = stage;
+      const float w0 = load_uniform(p.w0_s, w_at + kb), w1 = kGated ? load_uniform(p.w1_s, w_at + kb) : 0.f;
+      if (!landed) {
+        wait_dma_all();
+        workgroup_barrier();   // stage cur landed for every wave; stage cur ^ 1 no longer read
+      }
+      landed = false;
+      // the next block: the tile's, or the next tile's first (past the last tile the
+      // weights' last block again, into the stage no one reads again)
+      const bool last = kb + 1 == nkb;
+      const int kn = !last ? kb + 1 : more ? 0 : kb;
+      if (last && more) set_offsets(next);
+      if (dma_wave && (!last || more)) issue_a(kn, cur ^ 1);
+      // retire the scalar loads now: while one is outstanding every LDS wait
+      // would be a full drain
+      asm volatile("" ::"s"(w0), "s"(w1));
+      if (!live) {
+        issue_b(kn, cur ^ 1);
+        continue;
+      }
+      float sa[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sa[i] = sm.as[cur][wa + 16 * i + fr];
+      auto read_b = [&](int j) {
+        const int r = wb * 128 + 16 * j + fr;
+        return frag_from_lds(&sm.b[cur][r * kBlock], fq, r);
+      };
+      i32x8 bcur = read_b(0), bnext;
+      __builtin_amdgcn_sched_barrier(0);
+      i32x8 af[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t col = f0 + 4 * fq + i;
-        if (col < p.f) store_out(p.out, p.out_bf16, row * p.f + col, kGated ? gated(g[i], u[i]) : g[i]);
+        const int r = wa + 16 * i + fr;
+        af[i] = frag_from_lds(&sm.a[cur][r * kBlock], fq, r);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // the previous block's last rescale, while these reads are in flight
+#pragma unroll
+      for (int qp = 29; qp < 32; ++qp) rescale(qp);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j + 1 < 8) bnext = read_b(j + 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int q = 4 * j + i;
+          prt[q % 4] = mfma_e4m3_16x16x128(bcur, af[i], f32x4{0.f, 0.f, 0.f, 0.f});
+          // unconditional, so that no branch splits the unrolled loop
+          if (j == 2 && i == 0) issue_b(kn, cur ^ 1);
+          if (q == 3) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              sc[0][r] = sa[r] * w0;
+              sc[1][r] = sa[r] * w1;
+            }
+          }
+          if (q >= 3) rescale(q - 3);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (j + 1 < 8) bcur = bnext;
       }
     }
-  }
-  if (e == p.experts - 1)
-    for (int64_t row = end + fr; row < p.rows; row += 16)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (f0 + 4 * fq + i < p.f) store_out(p.out, p.out_bf16, row * p.f + f0 + 4 * fq + i, 0.0f);
+    for (int qp = 29; qp < 32; ++qp) rescale(qp);
+    // the next tile's first block is waited for before this tile's stores, which
+    // then drain while that block is computed
+    if (more) {
+      wait_dma_all();
+      workgroup_barrier();
+      landed = true;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = wa + 16 * i + fr;
+      if (r >= tile.left) continue;
+#pragma unroll
+      for (int j = 0; j < (kGated ? 4 : 8); ++j) {
+        const int64_t col = tile.f0 + (kGated ? 64 : 128) * wb + 16 * j + 4 * fq;
+        if (col < p.f) store_four(p, tile.row0 + r, col, kGated ? gated4(acc[i][j], acc[i][j + 4]) : acc[i][j]);
+      }
+    }
+    tile = next;
+  }
+  wait_dma_all();   // transfers past the end, before the workgroup's LDS is released
+  clear_behind(p, table.begin[p.experts], kBigThreads);
+}
+
+template <int kTokens>
+hipError_t launch_stream(ProductArgs p, bool gated, int cus, hipStream_t stream) {
+  const int features = gated ? kStreamRows / 2 : kStreamRows;
+  p.tiles_f = (int)((p.f + features - 1) / features);
+  const dim3 grid((unsigned)cus), block(StreamShape<kTokens>::kThreads);
+  if (gated)
+    hipLaunchKernelGGL((product_stream_kernel<true, kTokens>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((product_stream_kernel<false, kTokens>), grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_big(ProductArgs p, bool gated, int cus, hipStream_t stream) {
+  const int features = gated ? kBigTile / 2 : kBigTile;
+  p.tiles_f = (int)((p.f + features - 1) / features);
+  const dim3 grid((unsigned)cus), block(kBigThreads);
+  if (gated)
+    hipLaunchKernelGGL(product_big_kernel<true>, grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL(product_big_kernel<false>, grid, block, 0, stream, p);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -70,13 +607,32 @@ __global__ __launch_bounds__(256) void product_simple_kernel(const ProductArgs p
 hipError_t launch_expert_product(const uint8_t *a, const float *a_s, const int32_t *offsets, const uint8_t *w0,
                                  const float *w0_s, const uint8_t *w1, const float *w1_s, void *out, bool out_bf16,
                                  int64_t rows, int64_t experts, int64_t f, int64_t k, hipStream_t stream) {
-  const ProductArgs p = {a, a_s, offsets, w0, w1, w0_s, w1_s, out, rows, f, k, (int)experts, (int)(k / kBlock), out_bf16};
-  const dim3 grid((unsigned)((f + 63) / 64), (unsigned)experts), block(256);
-  if (w1)
-    hipLaunchKernelGGL(product_simple_kernel<true>, grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL(product_simple_kernel<false>, grid, block, 0, stream, p);
-  return hipGetLastError();
+  ProductArgs p = {};
+  p.a = a;
+  p.a_s = a_s;
+  p.offsets = offsets;
+  p.w0 = w0;
+  p.w1 = w1;
+  p.w0_s = w0_s;
+  p.w1_s = w1_s;
+  p.out = out;
+  p.rows = rows;
+  p.f = f;
+  p.k = k;
+  p.experts = (int)experts;
+  p.nkb = (int)(k / kBlock);
+  p.blocks_f = (int)((f + kBlock - 1) / kBlock);
+  p.out_bf16 = out_bf16;
+  p.vec = f % 4 == 0 && ((uintptr_t)out & (out_bf16 ? 7 : 15)) == 0;
+  int cus = current_device_cus();
+  if (cus <= 0) cus = 256;
+  const bool gated = w1 != nullptr;
+  // rows an expert, of the experts that can have any
+  const int64_t each = rows / min(rows, experts);
+  if (each <= 8) return launch_stream<16>(p, gated, cus, stream);
+  if (each <= 48) return launch_stream<64>(p, gated, cus, stream);
+  if (each <= 128) return launch_stream<128>(p, gated, cus, stream);
+  return launch_big(p, gated, cus, stream);
 }
 
 }  // namespace fp8bsq
