@@ -15,6 +15,9 @@
 #include "e4m3_tiles.h"
 #include "expert_launch.h"
 
+#include <type_traits>
+
+
 namespace fp8bsq {
 namespace {
 
@@ -28,7 +31,7 @@ struct ProductArgs {
   int64_t rows, f, k;
   int experts, nkb;
   int tiles_f, blocks_f;    // tiles and 128-wide blocks of the features
-  bool out_bf16, vec;
+  bool out_bf16, vec, vec8;   // four outputs of a row make one aligned store; eight bf16 ones do
 };
 
 // The experts' rows as the offsets give them, in order and inside the matrix
@@ -36,6 +39,13 @@ struct ProductArgs {
 struct Table {
   int begin[kMaxExperts + 1];   // expert's first row; the last: where the rows behind begin
   int first[kMaxExperts + 1];   // its first token tile; the last: their number
+};
+
+// The 256-row kernel's tiles of up to 128 rows, an expert's last, are a list of
+// their own behind the others: they take half as long, and in one list some
+// workgroups would get more of the long ones than others.
+struct SplitTable : Table {
+  int half[kMaxExperts + 1];    // experts before with such a tile; the last: their number
 };
 
 __device__ __forceinline__ int wave_max_scan(int v, int lane) {
@@ -57,12 +67,13 @@ __device__ __forceinline__ int wave_sum_scan(int v, int lane) {
 }
 
 // By all kThreads threads, kThreads experts at a time.
-template <int kThreads, int kTokens>
-__device__ __forceinline__ void build_table(const ProductArgs &p, Table &t) {
-  __shared__ int top[kThreads / 64], sum[kThreads / 64];
+template <int kThreads, int kTokens, typename T>
+__device__ __forceinline__ void build_table(const ProductArgs &p, T &t) {
+  constexpr bool kSplit = std::is_same<T, SplitTable>::value;
+  __shared__ int top[kThreads / 64], sum[kThreads / 64], halves[kThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   auto inside = [&](int v) { return min(max(v, 0), (int)p.rows); };
-  int rows_before = inside(p.offsets[0]), tiles_before = 0;
+  int rows_before = inside(p.offsets[0]), tiles_before = 0, halves_before = 0;
   for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
     const int e = e0 + threadIdx.x;
     const int m = wave_max_scan(e < p.experts ? inside(p.offsets[e + 1]) : 0, lane);
@@ -74,24 +85,35 @@ __device__ __forceinline__ void build_table(const ProductArgs &p, Table &t) {
       rows_before = max(rows_before, top[w]);
     }
     const int prev = __shfl_up(m, 1), begin = lane ? max(prev, before) : before, end = max(m, before);
-    const int tiles = (end - begin + kTokens - 1) / kTokens;
+    const int tiles = (end - begin + (kSplit ? kTokens / 2 : kTokens) - 1) / kTokens;
+    const int half = kSplit && end - begin > tiles * kTokens ? 1 : 0;
     const int s = wave_sum_scan(tiles, lane);
-    if (lane == 63) sum[wave] = s;
+    const uint64_t with_half = __ballot(half);
+    if (lane == 63) {
+      sum[wave] = s;
+      halves[wave] = __popcll(with_half);
+    }
     __syncthreads();
-    int at = tiles_before;
+    int at = tiles_before, half_at = halves_before;
     for (int w = 0; w < kThreads / 64; ++w) {
-      if (w < wave) at += sum[w];
+      if (w < wave) {
+        at += sum[w];
+        half_at += halves[w];
+      }
       tiles_before += sum[w];
+      halves_before += halves[w];
     }
     if (e < p.experts) {
       t.begin[e] = begin;
       t.first[e] = at + s - tiles;
+      if constexpr (kSplit) t.half[e] = half_at + __popcll(with_half & (((uint64_t)1 << lane) - 1));
     }
     __syncthreads();
   }
   if (threadIdx.x == 0) {
     t.begin[p.experts] = rows_before;
     t.first[p.experts] = tiles_before;
+    if constexpr (kSplit) t.half[p.experts] = halves_before;
   }
   __syncthreads();
 }
@@ -102,26 +124,51 @@ struct Tile {
   int64_t f0;
 };
 
-// Tile of turn `it`: workgroups are dealt round-robin to the eight XCDs, so turns
-// it, it + 8, ... get consecutive tiles of one XCD's contiguous share (they then
-// share its L2).  The same in every lane.
-template <int kTokens, int kFeatures>
-__device__ __forceinline__ Tile locate(const ProductArgs &p, const Table &t, uint32_t it, uint32_t ntiles, int lane) {
-  const uint32_t base = ntiles / 8, rest = ntiles % 8, xcd = it % 8;
-  const uint32_t tile = xcd * base + min(xcd, rest) + it / 8, q = tile / (uint32_t)p.tiles_f;
-  int e = 0;   // experts whose tiles end at or before token tile q
-  for (int e0 = 1; e0 <= p.experts; e0 += 64) {
-    const bool ended = e0 + lane <= p.experts && (uint32_t)t.first[min(e0 + lane, p.experts)] <= q;
-    e += __popcll(__ballot(ended));
-  }
-  e = __builtin_amdgcn_readfirstlane(e);
-  const int first = __builtin_amdgcn_readfirstlane(t.first[e]), tokens = __builtin_amdgcn_readfirstlane(t.first[e + 1]) - first;
-  const uint32_t rem = tile - (uint32_t)first * p.tiles_f;
-  const int tf = rem / tokens, ta = rem - (uint32_t)tf * tokens;
+// The last expert whose entry is at most q: with prefix sums, the one that q is in.
+// The same in every lane.
+__device__ __forceinline__ int expert_of(const int *prefix, int experts, uint32_t q, int lane) {
+  int e = 0;
+  for (int e0 = 1; e0 <= experts; e0 += 64)
+    e += __popcll(__ballot(e0 + lane <= experts && (uint32_t)prefix[min(e0 + lane, experts)] <= q));
+  return __builtin_amdgcn_readfirstlane(e);
+}
+
+// Position of turn `it` in a list: workgroups are dealt round-robin to the eight
+// XCDs, so turns it, it + 8, ... get consecutive positions of one XCD's contiguous
+// share (they then share its L2).
+__device__ __forceinline__ uint32_t xcd_share(uint32_t it, uint32_t all) {
+  const uint32_t xcd = it % 8;
+  return xcd * (all / 8) + min(xcd, all % 8) + it / 8;
+}
+
+// Tile of turn `it` below `ntiles`.  An expert's tiles run in groups of four token
+// tiles across the weights' tiles.
+template <int kTokens, int kFeatures, typename T>
+__device__ __forceinline__ Tile locate(const ProductArgs &p, const T &t, uint32_t it, uint32_t ntiles, int lane) {
   Tile r;
-  r.expert = e;
-  r.row0 = __builtin_amdgcn_readfirstlane(t.begin[e]) + ta * kTokens;
-  r.left = min(__builtin_amdgcn_readfirstlane(t.begin[e + 1]) - r.row0, kTokens);
+  uint32_t long_tiles = ntiles;
+  if constexpr (std::is_same<T, SplitTable>::value) {
+    long_tiles = (uint32_t)__builtin_amdgcn_readfirstlane(t.first[p.experts]) * (uint32_t)p.tiles_f;
+    if (it >= long_tiles) {
+      const uint32_t tile = xcd_share(it - long_tiles, ntiles - long_tiles), q = tile / (uint32_t)p.tiles_f;
+      r.expert = expert_of(t.half, p.experts, q, lane);
+      const int tokens = __builtin_amdgcn_readfirstlane(t.first[r.expert + 1]) - __builtin_amdgcn_readfirstlane(t.first[r.expert]);
+      r.row0 = __builtin_amdgcn_readfirstlane(t.begin[r.expert]) + tokens * kTokens;
+      r.left = __builtin_amdgcn_readfirstlane(t.begin[r.expert + 1]) - r.row0;
+      r.f0 = (int64_t)(tile - q * (uint32_t)p.tiles_f) * kFeatures;
+      return r;
+    }
+  }
+  const uint32_t tile = xcd_share(it, long_tiles);
+  r.expert = expert_of(t.first, p.experts, tile / (uint32_t)p.tiles_f, lane);
+  const int first = __builtin_amdgcn_readfirstlane(t.first[r.expert]);
+  const uint32_t tokens = (uint32_t)(__builtin_amdgcn_readfirstlane(t.first[r.expert + 1]) - first);
+  constexpr uint32_t kGroup = 4;
+  const uint32_t rem = tile - (uint32_t)first * (uint32_t)p.tiles_f, group = rem / (kGroup * (uint32_t)p.tiles_f);
+  const uint32_t across = min(tokens - group * kGroup, kGroup), idx = rem - group * kGroup * (uint32_t)p.tiles_f;
+  const uint32_t tf = idx / across;
+  r.row0 = __builtin_amdgcn_readfirstlane(t.begin[r.expert]) + (int)(group * kGroup + idx - tf * across) * kTokens;
+  r.left = min(__builtin_amdgcn_readfirstlane(t.begin[r.expert + 1]) - r.row0, kTokens);
   r.f0 = (int64_t)tf * kFeatures;
   return r;
 }
@@ -150,6 +197,22 @@ __device__ __forceinline__ void store_four(const ProductArgs &p, int64_t row, in
   } else {
     if (p.vec) store4<false, true>(p.out, at, v, 4); else store4<false, false>(p.out, at, v, left);
   }
+}
+
+// A row's outputs in two neighbouring 16-wide tiles, `col` the first's first: eight
+// consecutive bf16 a lane instead of four in each tile, so that a store covers 64
+// bytes of a row.  The swap leaves tile 0's columns in the even groups of 16 lanes
+// and tile 1's in the odd ones.
+__device__ __forceinline__ void store_pair(const ProductArgs &p, bool there, int64_t row, int64_t col, int fq, f32x4 v0, f32x4 v1) {
+  if (!p.vec8) {
+    if (there && col + 4 * fq < p.f) store_four(p, row, col + 4 * fq, v0);
+    if (there && col + 16 + 4 * fq < p.f) store_four(p, row, col + 16 + 4 * fq, v1);
+    return;
+  }
+  const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v0[0], v0[1]), pack_bf16x2(v1[0], v1[1]), false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v0[2], v0[3]), pack_bf16x2(v1[2], v1[3]), false, false);
+  const int64_t at = col + 16 * (fq & 1) + 8 * (fq >> 1);
+  if (there && at < p.f) *(u32x4 *)((uint16_t *)p.out + row * p.f + at) = u32x4{lo[0], hi[0], lo[1], hi[1]};
 }
 
 __device__ __forceinline__ f32x4 gated4(f32x4 g, f32x4 u) {
@@ -347,13 +410,16 @@ __global__ __launch_bounds__(StreamShape<kTokens>::kThreads) void product_stream
     auto finish = [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < S::kI; ++i) {
+        if (wa + 16 * i >= tile.left) break;
         const int r = wa + 16 * i + fr;
-        if (r >= tile.left) continue;
+        constexpr int kOut = kGated ? S::kJ / 2 : S::kJ;
+        auto value = [&](int j) { return kGated ? gated4(acc[i][j], acc[i][(j + S::kJ / 2) % S::kJ]) : acc[i][j]; };
+        const int64_t col = tile.f0 + (kGated ? kWaveRows / 2 : kWaveRows) * wb;
+        if constexpr (kOut == 1) {
+          if (r < tile.left && col + 4 * fq < p.f) store_four(p, tile.row0 + r, col + 4 * fq, value(0));
+        } else {
 #pragma unroll
-        for (int j = 0; j < (kGated ? S::kJ / 2 : S::kJ); ++j) {
-          const int64_t col = tile.f0 + (kGated ? kWaveRows / 2 : kWaveRows) * wb + 16 * j + 4 * fq;
-          if (col < p.f)
-            store_four(p, tile.row0 + r, col, kGated ? gated4(acc[i][j], acc[i][j + S::kJ / 2]) : acc[i][j]);
+          for (int j = 0; j < kOut; j += 2) store_pair(p, r < tile.left, tile.row0 + r, col + 16 * j, fq, value(j), value(j + 1));
         }
       }
     };
@@ -399,16 +465,16 @@ __global__ __launch_bounds__(StreamShape<kTokens>::kThreads) void product_stream
 // expert does not have skip their MFMAs: a tile of up to 128 rows keeps one wave a
 // SIMD.
 // ---------------------------------------------------------------------------
-template <bool kGated>
+template <bool kGated, bool kQuad>
 __global__ __launch_bounds__(kBigThreads) void product_big_kernel(const ProductArgs p) {
   constexpr int kFeatures = kGated ? kBigTile / 2 : kBigTile;
   struct Smem {
     uint8_t a[2][kBigTile * kBlock];
     uint8_t b[2][kBigTile * kBlock];
-    float as[2][kBigTile];
+    float as[2][kBigTile * (kQuad ? 4 : 1)];   // by block, or by [row][4 blocks]
   };
   __shared__ __attribute__((aligned(1024))) Smem sm;
-  __shared__ Table table;
+  __shared__ SplitTable table;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nkb = p.nkb;
@@ -420,7 +486,8 @@ __global__ __launch_bounds__(kBigThreads) void product_big_kernel(const ProductA
   const int dw = wave & 3, dr = lane >> 3, ds = lane & 7;
   const uint32_t lds_a = lds_addr(&sm.a[0][0]), lds_b = lds_addr(&sm.b[0][0]), lds_as = lds_addr(&sm.as[0][0]);
   build_table<kBigThreads, kBigTile>(p, table);
-  const uint32_t ntiles = (uint32_t)__builtin_amdgcn_readfirstlane(table.first[p.experts]) * (uint32_t)p.tiles_f;
+  const uint32_t ntiles = (uint32_t)(__builtin_amdgcn_readfirstlane(table.first[p.experts]) +
+                                     __builtin_amdgcn_readfirstlane(table.half[p.experts])) * (uint32_t)p.tiles_f;
 
   uint32_t a_off[8], b_off[4], s_off = 0;   // from the tile's own base
   const uint8_t *a_base = nullptr, *b_base = nullptr;
@@ -443,11 +510,16 @@ __global__ __launch_bounds__(kBigThreads) void product_big_kernel(const ProductA
       b_off[i] = (uint32_t)min(r, left - 1) * (uint32_t)p.k + ((ds ^ swz(row)) << 4);
     }
   };
+  int quad = 1;   // kQuad: the buffer that holds the newest four blocks' scales
   auto issue_a = [&](int kb, int s) {
     const uint8_t *ab = a_base + (int64_t)kb * kBlock;
 #pragma unroll
     for (int g = 0; g < 8; ++g) lds_dma16(ab, a_off[g], lds_a + s * (kBigTile * kBlock) + (8 * dw + g) * 1024);
-    lds_dma4(as_base + kb, s_off, lds_as + s * (kBigTile * 4) + dw * 256);
+    if (!kQuad) {
+      lds_dma4(as_base + kb, s_off, lds_as + s * (kBigTile * 4) + dw * 256);
+    } else if (kb % 4 == 0) {
+      lds_dma16(as_base + kb, s_off, lds_as + (quad ^ 1) * (kBigTile * 16) + dw * 1024);
+    }
   };
   auto issue_b = [&](int kb, int s) {
     const uint8_t *bb = b_base + (int64_t)kb * kBlock;
@@ -503,6 +575,7 @@ __global__ __launch_bounds__(kBigThreads) void product_big_kernel(const ProductA
       // weights' last block again, into the stage no one reads again)
       const bool last = kb + 1 == nkb;
       const int kn = !last ? kb + 1 : more ? 0 : kb;
+      if (kQuad && kb % 4 == 0) quad ^= 1;   // the four that begin here have landed
       if (last && more) set_offsets(next);
       if (dma_wave && (!last || more)) issue_a(kn, cur ^ 1);
       // retire the scalar loads now: while one is outstanding every LDS wait
@@ -514,7 +587,8 @@ __global__ __launch_bounds__(kBigThreads) void product_big_kernel(const ProductA
       }
       float sa[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sa[i] = sm.as[cur][wa + 16 * i + fr];
+      for (int i = 0; i < 4; ++i)
+        sa[i] = kQuad ? sm.as[quad][(wa + 16 * i + fr) * 4 + kb % 4] : sm.as[cur][wa + 16 * i + fr];
       auto read_b = [&](int j) {
         const int r = wb * 128 + 16 * j + fr;
         return frag_from_lds(&sm.b[cur][r * kBlock], fq, r);
@@ -565,13 +639,13 @@ __global__ __launch_bounds__(kBigThreads) void product_big_kernel(const ProductA
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      if (wa + 16 * i >= tile.left) break;
       const int r = wa + 16 * i + fr;
-      if (r >= tile.left) continue;
 #pragma unroll
-      for (int j = 0; j < (kGated ? 4 : 8); ++j) {
-        const int64_t col = tile.f0 + (kGated ? 64 : 128) * wb + 16 * j + 4 * fq;
-        if (col < p.f) store_four(p, tile.row0 + r, col, kGated ? gated4(acc[i][j], acc[i][j + 4]) : acc[i][j]);
-      }
+      for (int j = 0; j < (kGated ? 4 : 8); j += 2)
+        store_pair(p, r < tile.left, tile.row0 + r, tile.f0 + (kGated ? 64 : 128) * wb + 16 * j, fq,
+                   kGated ? gated4(acc[i][j], acc[i][(j + 4) % 8]) : acc[i][j],
+                   kGated ? gated4(acc[i][j + 1], acc[i][(j + 5) % 8]) : acc[i][j + 1]);
     }
     tile = next;
   }
@@ -595,10 +669,18 @@ hipError_t launch_big(ProductArgs p, bool gated, int cus, hipStream_t stream) {
   const int features = gated ? kBigTile / 2 : kBigTile;
   p.tiles_f = (int)((p.f + features - 1) / features);
   const dim3 grid((unsigned)cus), block(kBigThreads);
-  if (gated)
-    hipLaunchKernelGGL(product_big_kernel<true>, grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL(product_big_kernel<false>, grid, block, 0, stream, p);
+  const bool quad = p.nkb % 4 == 0 && ((uintptr_t)p.a_s & 15) == 0;
+  if (gated) {
+    if (quad)
+      hipLaunchKernelGGL((product_big_kernel<true, true>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((product_big_kernel<true, false>), grid, block, 0, stream, p);
+  } else {
+    if (quad)
+      hipLaunchKernelGGL((product_big_kernel<false, true>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((product_big_kernel<false, false>), grid, block, 0, stream, p);
+  }
   return hipGetLastError();
 }
 
@@ -623,15 +705,16 @@ hipError_t launch_expert_product(const uint8_t *a, const float *a_s, const int32
   p.nkb = (int)(k / kBlock);
   p.blocks_f = (int)((f + kBlock - 1) / kBlock);
   p.out_bf16 = out_bf16;
+  p.vec8 = out_bf16 && f % 8 == 0 && ((uintptr_t)out & 15) == 0;
   p.vec = f % 4 == 0 && ((uintptr_t)out & (out_bf16 ? 7 : 15)) == 0;
   int cus = current_device_cus();
   if (cus <= 0) cus = 256;
   const bool gated = w1 != nullptr;
   // rows an expert, of the experts that can have any
   const int64_t each = rows / min(rows, experts);
-  if (each <= 8) return launch_stream<16>(p, gated, cus, stream);
+  if (each <= 12) return launch_stream<16>(p, gated, cus, stream);
   if (each <= 48) return launch_stream<64>(p, gated, cus, stream);
-  if (each <= 128) return launch_stream<128>(p, gated, cus, stream);
+  if (each <= 96) return launch_stream<128>(p, gated, cus, stream);
   return launch_big(p, gated, cus, stream);
 }
 
