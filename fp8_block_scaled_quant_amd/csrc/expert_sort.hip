@@ -21,6 +21,7 @@ namespace fp8bsq {
 namespace {
 
 constexpr int kMaxWaves = 16;
+constexpr int64_t kFew = 16;            // choices that one wave counts over
 constexpr int64_t kSingle = 4096;       // choices of a single workgroup
 constexpr int64_t kChunk = 2048;        // choices a workgroup, at least, of several
 constexpr int64_t kMaxGroups = 256;     // whose counts every workgroup reads
@@ -52,37 +53,67 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sort_count_kernel(const SortAr
 
 template <bool kWide>
 __global__ __launch_bounds__(64 * kMaxWaves) void sort_place_kernel(const SortArgs p) {
-  // [wave][num + 1] next rows, then [num + 1] all choices' counts and where buckets begin
+  // [wave][num + 1] counts, then places; [num + 1] all choices' counts, then where
+  // buckets begin; [num + 1] choices in the workgroups before
   extern __shared__ uint32_t lds[];
   const int buckets = p.num + 1, waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t *mine = lds + wave * buckets, *first = lds + waves * buckets;
-  for (int b = threadIdx.x; b < waves * buckets; b += blockDim.x) lds[b] = 0;
-  __syncthreads();
+  uint32_t *mine = lds + wave * buckets, *first = lds + waves * buckets, *before = first + buckets;
 
   const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(p.n, begin + p.chunk);
   const int64_t per = ((end - begin + blockDim.x - 1) / blockDim.x) * 64;   // choices a wave, whole rounds
   const int64_t wbegin = begin + wave * per, wend = min(end, wbegin + per);
-  for (int64_t c = wbegin + lane; c < wend; c += 64) atomicAdd(&mine[bucket_of<kWide>(p, c)], 1u);
+  // the buckets of the wave's first rounds stay in registers
+  constexpr int kHeld = 4;
+  int held[kHeld];
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r) {
+    const int64_t c = wbegin + 64 * r + lane;
+    held[r] = c < wend ? bucket_of<kWide>(p, c) : -1;
+  }
+  for (int b = threadIdx.x; b < (waves + 2) * buckets; b += blockDim.x) lds[b] = 0;
   __syncthreads();
 
-  // each bucket's choices: of the waves before (kept), of the workgroups before, of all
-  for (int b = threadIdx.x; b < buckets; b += blockDim.x) {
-    uint32_t before = 0, all = 0;
-    if (p.groups > 1) {
-#pragma unroll 8
-      for (int g = 0; g < p.groups; ++g) {
-        const uint32_t v = p.counts[(int64_t)g * buckets + b];
-        before += g < (int)blockIdx.x ? v : 0;
-        all += v;
+  // each bucket's choices in the workgroups before this one, and in all: shares of
+  // the workgroups by as many threads as there are, several loads in flight each
+  if (p.groups > 1) {
+    const int parts = max(1, (int)blockDim.x / buckets), share = (p.groups + parts - 1) / parts;
+    for (int i = threadIdx.x; i < parts * buckets; i += blockDim.x) {
+      const int part = i / buckets, b = i - part * buckets, g1 = min(p.groups, (part + 1) * share);
+      uint32_t prior = 0, all = 0;
+      constexpr int kTogether = 12;
+      for (int g0 = part * share; g0 < g1; g0 += kTogether) {
+        uint32_t v[kTogether];
+#pragma unroll
+        for (int g = 0; g < kTogether; ++g) v[g] = p.counts[(int64_t)min(g0 + g, g1 - 1) * buckets + b];
+#pragma unroll
+        for (int g = 0; g < kTogether; ++g) {
+          prior += g0 + g < min(g1, (int)blockIdx.x) ? v[g] : 0;
+          all += g0 + g < g1 ? v[g] : 0;
+        }
       }
+      atomicAdd(&first[b], all);
+      atomicAdd(&before[b], prior);
     }
-    for (int w = 0; w < waves; ++w) {
-      const uint32_t v = lds[w * buckets + b];
-      lds[w * buckets + b] = before;
-      before += v;
+  }
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r)
+    if (held[r] >= 0) atomicAdd(&mine[held[r]], 1u);
+  for (int64_t c = wbegin + 64 * kHeld + lane; c < wend; c += 64) atomicAdd(&mine[bucket_of<kWide>(p, c)], 1u);
+  __syncthreads();
+
+  // the waves' counts to the numbers of choices before theirs
+  for (int b = threadIdx.x; b < buckets; b += blockDim.x) {
+    uint32_t v[kMaxWaves], at = before[b];
+#pragma unroll
+    for (int w = 0; w < kMaxWaves; ++w) v[w] = lds[min(w, waves - 1) * buckets + b];
+#pragma unroll
+    for (int w = 0; w < kMaxWaves; ++w) {
+      if (w >= waves) break;
+      lds[w * buckets + b] = at;
+      at += v[w];
     }
-    first[b] = p.groups > 1 ? all : before;
+    if (p.groups == 1) first[b] = at;
   }
   __syncthreads();
 
@@ -107,25 +138,58 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sort_place_kernel(const SortAr
   }
   __syncthreads();
 
+  constexpr int kMaxBits = 11;
+  static_assert(kMaxExperts < 1 << kMaxBits, "a bucket's number");
   const int bits = 32 - __builtin_clz(p.num);
-  for (int64_t c0 = wbegin; c0 < wend; c0 += 64) {
-    const int64_t c = c0 + lane;
-    const bool there = c < wend;
-    const int b = there ? bucket_of<kWide>(p, c) : 0;
-    uint64_t same = __ballot(there);
-    for (int i = 0; i < bits; ++i) {
-      const uint64_t set = __ballot((b >> i) & 1);
-      same &= (b >> i) & 1 ? set : ~set;
+  auto place = [&](int64_t c, int b) {   // b below 0: no choice
+    const uint64_t there = __ballot(b >= 0);
+    uint32_t lo = (uint32_t)there, hi = (uint32_t)(there >> 32);
+#pragma unroll
+    for (int i = 0; i < kMaxBits; ++i) {
+      if (i >= bits) break;
+      const uint32_t bit = (uint32_t)(b << (31 - i) >> 31);   // all ones where it is set
+      const uint64_t set = __ballot(bit != 0);
+      lo &= ~((uint32_t)set ^ bit);
+      hi &= ~((uint32_t)(set >> 32) ^ bit);
     }
-    if (there) {
-      const uint32_t place = (uint32_t)__popcll(same & (((uint64_t)1 << lane) - 1));
+    const uint64_t same = (uint64_t)hi << 32 | lo;
+    if (b >= 0) {
+      const uint32_t below = (uint32_t)__popcll(same & (((uint64_t)1 << lane) - 1));
       const uint32_t next = mine[b];
-      const uint32_t row = first[b] + next + place;
+      const uint32_t row = first[b] + next + below;
       p.rows[c] = (int32_t)(b < p.num ? row : ~row);
       p.choices[row] = (int32_t)c;
       // after every lane's read above: a wave's LDS accesses are executed in order
-      if (place == 0) mine[b] = next + (uint32_t)__popcll(same);
+      if (below == 0) mine[b] = next + (uint32_t)__popcll(same);
     }
+  };
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r)
+    if (wbegin + 64 * r < wend) place(wbegin + 64 * r + lane, held[r]);
+  for (int64_t c = wbegin + 64 * kHeld + lane; c - lane < wend; c += 64) place(c, c < wend ? bucket_of<kWide>(p, c) : -1);
+}
+
+// Up to kFew choices: every wave holds them all, and a choice's row and an expert's
+// offset are counts over them.
+template <bool kWide>
+__global__ __launch_bounds__(256) void sort_few_kernel(const SortArgs p) {
+  const int lane = threadIdx.x & 63, n = (int)p.n;
+  const int mine = lane < n ? bucket_of<kWide>(p, lane) : 0x7FFFFFFF;
+  if (threadIdx.x < 64) {
+    int row = 0;
+    for (int c = 0; c < n; ++c) {
+      const int b = __builtin_amdgcn_readlane(mine, c);
+      row += b < mine || (b == mine && c < lane) ? 1 : 0;
+    }
+    if (lane < n) {
+      p.rows[lane] = mine < p.num ? row : ~row;
+      p.choices[row] = lane;
+    }
+  }
+  for (int e = threadIdx.x; e <= p.num; e += blockDim.x) {
+    int below = 0;
+    for (int c = 0; c < n; ++c) below += __builtin_amdgcn_readlane(mine, c) < e ? 1 : 0;
+    p.offsets[e] = below;
   }
 }
 
@@ -140,7 +204,6 @@ SortPlan sort_plan(int64_t n) {
     p.groups = 1;
     p.chunk = n;
     p.waves = (int)min((n + 63) / 64, (int64_t)kMaxWaves);
-    if (p.waves == 0) p.waves = 1;   // no choices: the offsets all the same
     return p;
   }
   const int64_t groups = min((n + kChunk - 1) / kChunk, kMaxGroups);
@@ -164,6 +227,13 @@ hipError_t launch_expert_sort(const void *experts, bool wide, int64_t n, int64_t
   const SortArgs p = {experts, n, plan.chunk, (int)num_experts, plan.groups, offsets, rows, choices, (uint32_t *)workspace};
   const size_t table = (size_t)(num_experts + 1) * sizeof(uint32_t);
   const dim3 grid((unsigned)plan.groups), block(64 * plan.waves);
+  if (n <= kFew) {
+    if (wide)
+      hipLaunchKernelGGL(sort_few_kernel<true>, dim3(1), dim3(256), 0, stream, p);
+    else
+      hipLaunchKernelGGL(sort_few_kernel<false>, dim3(1), dim3(256), 0, stream, p);
+    return hipGetLastError();
+  }
   if (plan.groups > 1) {
     if (wide)
       hipLaunchKernelGGL(sort_count_kernel<true>, grid, block, table, stream, p);
@@ -173,9 +243,9 @@ hipError_t launch_expert_sort(const void *experts, bool wide, int64_t n, int64_t
     if (e != hipSuccess) return e;
   }
   if (wide)
-    hipLaunchKernelGGL(sort_place_kernel<true>, grid, block, (plan.waves + 1) * table, stream, p);
+    hipLaunchKernelGGL(sort_place_kernel<true>, grid, block, (plan.waves + 2) * table, stream, p);
   else
-    hipLaunchKernelGGL(sort_place_kernel<false>, grid, block, (plan.waves + 1) * table, stream, p);
+    hipLaunchKernelGGL(sort_place_kernel<false>, grid, block, (plan.waves + 2) * table, stream, p);
   return hipGetLastError();
 }
 

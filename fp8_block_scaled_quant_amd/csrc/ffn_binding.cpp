@@ -6,6 +6,7 @@
 //
 // Wrong types raise TypeError, wrong shapes or devices ValueError, and a status
 // of the library its Fp8Error.
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -291,7 +292,14 @@ int require_weights(const std::optional<Tensor> &weights, const Tensor &rows, c1
 
 const void *data_or_null(const std::optional<Tensor> &t) { return t ? t->data_ptr() : nullptr; }
 
-Tensor expert_dispatch(const Tensor &x, const Tensor &rows) {
+// Whether autograd has to see an operation on t: a gradient is asked for, or a
+// forward-mode tangent comes along (which the function refuses and a plain call
+// would drop).
+bool tracked(const Tensor &t) { return (at::GradMode::is_enabled() && t.requires_grad()) || t._fw_grad(0).defined(); }
+
+// None where `ask` and autograd has to see the call.
+py::object expert_dispatch(const Tensor &x, const Tensor &rows, bool ask) {
+  if (ask && tracked(x)) return py::none();
   const c10::Device device = x.device();
   for (const Tensor *t : {&x, &rows}) require_gpu(*t, device);
   const int dtype = dtype_of(x);
@@ -302,7 +310,7 @@ Tensor expert_dispatch(const Tensor &x, const Tensor &rows) {
   const c10::DeviceGuard guard(device);
   const Tensor y = empty({c.tokens * c.top_k, h}, x.scalar_type(), device);
   check_status(fp8bsq_expert_dispatch(x.data_ptr(), dtype, c.rows, c.tokens, c.top_k, h, y.data_ptr(), stream_of(device)));
-  return y;
+  return py::cast(y);
 }
 
 py::tuple expert_dispatch_quant(const Tensor &x, const Tensor &rows, int scale_fmt) {
@@ -321,7 +329,8 @@ py::tuple expert_dispatch_quant(const Tensor &x, const Tensor &rows, int scale_f
   return py::make_tuple(y, s);
 }
 
-Tensor expert_combine(const Tensor &y, const Tensor &rows, const std::optional<Tensor> &weights) {
+py::object expert_combine(const Tensor &y, const Tensor &rows, const std::optional<Tensor> &weights, bool ask) {
+  if (ask && (tracked(y) || (weights && tracked(*weights)))) return py::none();
   const c10::Device device = y.device();
   for (const Tensor *t : {&y, &rows}) require_gpu(*t, device);
   const int dtype = dtype_of(y);
@@ -334,7 +343,7 @@ Tensor expert_combine(const Tensor &y, const Tensor &rows, const std::optional<T
   const Tensor out = empty(with_last(rows, h), y.scalar_type(), device);
   check_status(fp8bsq_expert_combine(y.data_ptr(), dtype, c.rows, data_or_null(weights), w_dtype, c.tokens, c.top_k, h,
                                      out.data_ptr(), stream_of(device)));
-  return out;
+  return py::cast(out);
 }
 
 py::tuple expert_combine_backward(const Tensor &dout, const Tensor &y, const Tensor &rows,

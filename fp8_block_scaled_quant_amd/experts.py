@@ -11,7 +11,6 @@ kernels; tensors on the CPU raise.
 from typing import NamedTuple
 
 import torch
-from torch.autograd import forward_ad
 
 from . import _DTYPE, _ffn_lib, act_quant, weight_quant
 from .ffn import _format, _out
@@ -53,7 +52,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, rows):
         ctx.save_for_backward(rows)
-        return _ffn_lib.ext().expert_dispatch(x, rows)
+        return _ffn_lib.ext().expert_dispatch(x, rows, False)
 
     @staticmethod
     def backward(ctx, dy):
@@ -64,7 +63,7 @@ class _Sum(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, rows):
         ctx.save_for_backward(rows)
-        return _ffn_lib.ext().expert_combine(y, rows, None)
+        return _ffn_lib.ext().expert_combine(y, rows, None, False)
 
     @staticmethod
     def backward(ctx, dout):
@@ -75,7 +74,7 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, rows, weights):
         ctx.save_for_backward(y, rows, weights)
-        return _ffn_lib.ext().expert_combine(y, rows, weights)
+        return _ffn_lib.ext().expert_combine(y, rows, weights, False)
 
     @staticmethod
     def backward(ctx, dout):
@@ -86,22 +85,14 @@ class _Combine(torch.autograd.Function):
         return dy, None, dweights
 
 
-def _differentiable(*tensors):
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
-        return True
-    # a forward-mode tangent: the function refuses it, a plain call would drop it
-    return any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
-
-
 def expert_dispatch(x: torch.Tensor, rows: torch.Tensor) -> torch.Tensor:
     """The tokens' rows ``x`` [..., H] (bf16 or fp32) in sorted order, [n, H]: row
     ``rows[t, j]`` is ``x[t]``; the rows behind the experts' are zero.
 
     ``rows`` [..., top_k] is ``expert_sort``'s.  Differentiable, to any order.
     """
-    if _differentiable(x):
-        return _Dispatch.apply(x, rows)
-    return _ffn_lib.ext().expert_dispatch(x, rows)
+    y = _ffn_lib.ext().expert_dispatch(x, rows, True)
+    return _Dispatch.apply(x, rows) if y is None else y   # None: autograd has to see the call
 
 
 def expert_dispatch_quant(x: torch.Tensor, rows: torch.Tensor, scale_fmt=None):
@@ -118,11 +109,10 @@ def expert_combine(y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor = 
     out, whatever their rows hold.  Differentiable in ``y`` and ``weights`` (with
     weights, to first order).
     """
-    if weights is None:
-        return _Sum.apply(y, rows) if _differentiable(y) else _ffn_lib.ext().expert_combine(y, rows, None)
-    if _differentiable(y, weights):
-        return _Combine.apply(y, rows, weights)
-    return _ffn_lib.ext().expert_combine(y, rows, weights)
+    out = _ffn_lib.ext().expert_combine(y, rows, weights, True)
+    if out is not None:
+        return out
+    return _Sum.apply(y, rows) if weights is None else _Combine.apply(y, rows, weights)
 
 
 def expert_combine_backward(dout: torch.Tensor, y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor = None,
