@@ -8,13 +8,14 @@
 // the launch depends on sizes only.  Within an expert the tiles of one piece of
 // weight follow each other, so that it comes from HBM once.
 //
-// Two kernels: tiles of up to 128 rows by 128 rows of weights, with transfers many
+// Two kernels: tiles of 16 or 64 rows by 128 rows of weights, with transfers many
 // blocks ahead, for few rows an expert (bound by the weights' bytes), and of 256 by
 // 256, for many (bound by the matrix cores).
 #include "device_cus.h"
 #include "e4m3_tiles.h"
 #include "expert_launch.h"
 
+#include <math.h>
 #include <type_traits>
 
 
@@ -150,8 +151,10 @@ __device__ __forceinline__ Tile locate(const ProductArgs &p, const T &t, uint32_
   if constexpr (std::is_same<T, SplitTable>::value) {
     long_tiles = (uint32_t)__builtin_amdgcn_readfirstlane(t.first[p.experts]) * (uint32_t)p.tiles_f;
     if (it >= long_tiles) {
+      // the last expert first: its weights were read last, and may still be in a cache
       const uint32_t tile = xcd_share(it - long_tiles, ntiles - long_tiles), q = tile / (uint32_t)p.tiles_f;
-      r.expert = expert_of(t.half, p.experts, q, lane);
+      const uint32_t halves = (uint32_t)__builtin_amdgcn_readfirstlane(t.half[p.experts]);
+      r.expert = expert_of(t.half, p.experts, halves - 1 - q, lane);
       const int tokens = __builtin_amdgcn_readfirstlane(t.first[r.expert + 1]) - __builtin_amdgcn_readfirstlane(t.first[r.expert]);
       r.row0 = __builtin_amdgcn_readfirstlane(t.begin[r.expert]) + tokens * kTokens;
       r.left = __builtin_amdgcn_readfirstlane(t.begin[r.expert + 1]) - r.row0;
@@ -236,15 +239,15 @@ constexpr int kStreamRows = 128;   // of weights, a tile
 
 template <int kTokens>
 struct StreamShape {
-  static constexpr int kSlots = kTokens == 128 ? 4 : kTokens == 64 ? 5 : 7;
-  static constexpr int kMovers = kTokens == 128 ? 1 : kTokens == 64 ? 2 : 4;   // of weights; one more of a
+  static constexpr int kSlots = kTokens == 64 ? 5 : 7;
+  static constexpr int kMovers = kTokens == 64 ? 2 : 4;    // of weights; one more of a
   static constexpr int kThreads = 64 * (4 + kMovers + 1);
-  static constexpr int kAcross = kTokens >= 64 ? 2 : 4;    // compute waves along the weights' rows
+  static constexpr int kAcross = kTokens == 64 ? 2 : 4;    // compute waves along the weights' rows
   static constexpr int kI = kTokens / 16 / (4 / kAcross);  // MFMA tiles of a wave along the tokens,
   static constexpr int kJ = kStreamRows / 16 / kAcross;    // and along the weights
-  static constexpr int kScales = kTokens < 64 ? 64 : kTokens;
+  static constexpr int kScales = 64;                       // a's, a block; those past the tile's rows are copies
   static constexpr int kSlotBytes = (kTokens + kStreamRows) * kBlock + kScales * 4;
-  static constexpr int kDmaA = kTokens / 8 + kScales / 64, kDmaB = 16 / kMovers;   // transfers a block and mover
+  static constexpr int kDmaA = kTokens / 8 + 1, kDmaB = 16 / kMovers;   // transfers a block and mover
   static_assert((kSlots - 1) * (kDmaA > kDmaB ? kDmaA : kDmaB) < 64, "the wait counter's range");
 };
 
@@ -294,7 +297,7 @@ __global__ __launch_bounds__(StreamShape<kTokens>::kThreads) void product_stream
     // lane p of an 8-row group fills chunk slot p % 8 of row p / 8; rows past an
     // edge re-read the last one
     if (wave == 4) {
-      uint32_t off[kTokens / 8], s_off[S::kScales / 64];
+      uint32_t off[kTokens / 8], s_off = 0;
       const uint8_t *base = nullptr;
       const float *scales = nullptr;
       drive(
@@ -304,17 +307,14 @@ __global__ __launch_bounds__(StreamShape<kTokens>::kThreads) void product_stream
               const int row = 8 * i + dr;
               off[i] = (uint32_t)min(row, t.left - 1) * (uint32_t)p.k + ((ds ^ swz(row)) << 4);
             }
-#pragma unroll
-            for (int i = 0; i < S::kScales / 64; ++i) s_off[i] = (uint32_t)min(64 * i + lane, t.left - 1) * (uint32_t)nkb * 4;
+            s_off = (uint32_t)min(lane, t.left - 1) * (uint32_t)nkb * 4;
             base = p.a + (int64_t)t.row0 * p.k;
             scales = p.a_s + (int64_t)t.row0 * nkb;
           },
           [&](int64_t kb, uint32_t to) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < kTokens / 8; ++i) lds_dma16(base + kb * kBlock, off[i], to + i * 1024);
-#pragma unroll
-            for (int i = 0; i < S::kScales / 64; ++i)
-              lds_dma4(scales + kb, s_off[i], to + (kTokens + kStreamRows) * kBlock + i * 256);
+            lds_dma4(scales + kb, s_off, to + (kTokens + kStreamRows) * kBlock);
           },
           [&]() __attribute__((always_inline)) { asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * S::kDmaA) : "memory"); });
     } else {
@@ -684,6 +684,30 @@ hipError_t launch_big(ProductArgs p, bool gated, int cus, hipStream_t stream) {
   return hipGetLastError();
 }
 
+enum class Shape { kFew, kSome, kMany };
+
+// By the rows an expert has on average, which is all that the host knows.  Up to
+// eight, nearly no expert has more than 16 (us, tiles of 16 and 64 rows: 64 experts of
+// 2 x 2048 x 7168 with 4 rows each 294 and 299, 12 rows 312 and 314; 8 experts 36.0
+// and 36.9, 12 rows 50 and 38).  From there on the cheaper of 64 and 256 rows by the
+// time of a round of tiles on all CUs, so much per block of 128 and so much besides,
+// or by the weights' bytes; a partial tile an expert is half of one more on average.
+// Measured (64 and 256 rows): 64 experts of 2 x 2048 x 7168 with 64 rows 429 and 484,
+// 128 rows 637 and 507; of 2300 x 1408 with 64 rows 50 and 63, 128 rows 79 and 70;
+// 16 of 2 x 512 x 1024 with 128 rows 13.0 and 17.4, 384 rows 22.1 and 18.2.
+Shape product_shape(int64_t rows, int64_t experts, int64_t f, int64_t k, bool gated, int cus) {
+  const double active = (double)min(rows, experts), each = (double)rows / active, nkb = (double)(k / kBlock);
+  if (each <= 8) return Shape::kFew;
+  auto rounds = [&](double rows_a_tile, double features) {
+    const double tokens = each / rows_a_tile + 0.5;
+    return ceil(active * (tokens > 1.0 ? tokens : 1.0) * ceil((double)f / features) / cus);
+  };
+  const double weights_us = active * (double)f * (double)k * (gated ? 2.0 : 1.0) / 5.1e6;
+  const double some_us = rounds(64, gated ? 64 : 128) * (nkb * 0.48 + 1.7);
+  const double many_us = rounds(256, gated ? 128 : 256) * (nkb * (each <= 128 ? 1.2 : 1.8) + 7.0);
+  return many_us < some_us && weights_us < some_us ? Shape::kMany : Shape::kSome;
+}
+
 }  // namespace
 
 hipError_t launch_expert_product(const uint8_t *a, const float *a_s, const int32_t *offsets, const uint8_t *w0,
@@ -710,12 +734,11 @@ hipError_t launch_expert_product(const uint8_t *a, const float *a_s, const int32
   int cus = current_device_cus();
   if (cus <= 0) cus = 256;
   const bool gated = w1 != nullptr;
-  // rows an expert, of the experts that can have any
-  const int64_t each = rows / min(rows, experts);
-  if (each <= 12) return launch_stream<16>(p, gated, cus, stream);
-  if (each <= 48) return launch_stream<64>(p, gated, cus, stream);
-  if (each <= 96) return launch_stream<128>(p, gated, cus, stream);
-  return launch_big(p, gated, cus, stream);
+  switch (product_shape(rows, experts, f, k, gated, cus)) {
+    case Shape::kFew: return launch_stream<16>(p, gated, cus, stream);
+    case Shape::kSome: return launch_stream<64>(p, gated, cus, stream);
+    default: return launch_big(p, gated, cus, stream);
+  }
 }
 
 }  // namespace fp8bsq
