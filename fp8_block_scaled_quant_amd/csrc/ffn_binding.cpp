@@ -240,6 +240,14 @@ Tensor clip(const py::list &grads, const std::optional<py::list> &outs, double m
 // Experts
 // ---------------------------------------------------------------------------
 
+// A contiguous tensor of its own over part of a 1-D one's storage.
+Tensor piece(const Tensor &all, int64_t offset, at::IntArrayRef shape) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(offset);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 py::tuple expert_sort(const Tensor &experts, int64_t num_experts) {
   const c10::Device device = experts.device();
   require_gpu(experts, device);
@@ -249,8 +257,10 @@ py::tuple expert_sort(const Tensor &experts, int64_t num_experts) {
   if (num_experts <= 0) value("num_experts must be positive");
   const int64_t n = experts.numel();
   const c10::DeviceGuard guard(device);
-  const Tensor offsets = empty({num_experts + 1}, at::kInt, device), rows = empty(experts.sizes(), at::kInt, device),
-               choices = empty({n}, at::kInt, device);
+  // one allocation for the three: the call is shorter than two more
+  const Tensor all = empty({num_experts + 1 + 2 * n}, at::kInt, device);
+  const Tensor offsets = piece(all, 0, {num_experts + 1}), rows = piece(all, num_experts + 1, experts.sizes()),
+               choices = piece(all, num_experts + 1 + n, {n});
   const size_t bytes = fp8bsq_expert_sort_workspace(n, num_experts);
   Tensor ws;
   if (bytes) ws = workspace(bytes, device);
