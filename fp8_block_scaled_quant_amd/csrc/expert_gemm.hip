@@ -234,6 +234,11 @@ __device__ __forceinline__ f32x4 gated4(f32x4 g, f32x4 u) {
 // (16 KB a block) at HBM's rate, also where tiles are short.  One barrier a block
 // hands the ring on; a block's fragments are read to registers while the block
 // before it feeds the MFMAs.
+//
+// Measured: one token at eight experts of 2 x 2048 x 7168 43.5 us, 235 MB at 5.4 TB/s
+// (a 1 GiB copy: 5.1; a wave per 16 features without LDS: 83 us); 8 rows each at 64
+// experts 316 us, 1.9 GB at 6.0 TB/s; 66 rows each, unevenly, at 64 of 2300 x 1408 59
+// us, 3.9 TB/s: experts above 64 rows take a second tile, whose weights L2 holds.
 // ---------------------------------------------------------------------------
 constexpr int kStreamRows = 128;   // of weights, a tile
 
@@ -464,6 +469,17 @@ __global__ __launch_bounds__(StreamShape<kTokens>::kThreads) void product_stream
 // The rescale of an MFMA's partial runs three MFMAs behind it.  Waves whose rows an
 // expert does not have skip their MFMAs: a tile of up to 128 rows keeps one wave a
 // SIMD.
+//
+// Measured, 2 x 2048 x 7168: 512 rows at each of 64 experts 902-927 us, 2.1 PFLOP/s;
+// 1024 rows 1691-1742, 2.2-2.3; 4096 x 4 choices of 32 experts, unevenly, 535-580 us,
+// 1.7 PFLOP/s (four rounds of long tiles and one of short ones, whose weights come
+// from HBM again; the matrix cores are busy 43% of the cycles, at 2.05 GHz).  7168 x
+// 2048: 512 rows 503-521 us, 4096 x 4 choices 287-296.  What it took (902 and 503):
+// scales of four blocks a transfer and the tiles' order (1068 and 592 without), 16
+// byte stores (909 and 537 with 8).  What was measured slower: the weights' transfers
+// one to two MFMA columns earlier or later (by up to 8%), a's by all eight waves (2-8%),
+// lines touched three blocks ahead (8-12%), short tiles on all eight waves, 64 x 64
+// each (registers spill: 8-20%).
 // ---------------------------------------------------------------------------
 template <bool kGated, bool kQuad>
 __global__ __launch_bounds__(kBigThreads) void product_big_kernel(const ProductArgs p) {

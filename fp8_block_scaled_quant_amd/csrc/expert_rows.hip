@@ -8,7 +8,14 @@
 //
 // All four go by the token: its own row is read (or written) once, the rows of its
 // choices are written (or read) once, and nothing is added up by atomics.  Each is
-// bound by memory.  Rows that nothing in L2's reach reads next are moved past it.  A row number outside the sorted rows touches nothing.
+// bound by memory; measured, in bytes that must move against a 1 GiB copy's 5.1 TB/s:
+//   dispatch_quant    8192 x 8 rows of 7168, bf16: 118 us, 5.1 TB/s
+//   dispatch          1333 x 3 rows of 1001 fp32: 5.2 us, 4.1 TB/s
+//   combine           4096 x 8 choices, half taking part, of 2048 bf16: 13.8 us, 6.1 TB/s
+//   combine_backward  4096 x 8 rows of 4096 bf16: 113 us, 5.0 TB/s
+// Rows that are written, and those that the backward pass reads, go past the caches
+// (dispatch 6.2 us otherwise, combine_backward 122); combine's reads do not (15.6).
+// A row number outside the sorted rows touches nothing.
 #include "expert_launch.h"
 #include "quant_block.h"
 
@@ -33,7 +40,7 @@ struct RowArgs {
 
 constexpr int kGroup = 8;   // choices whose rows are in flight together
 
-// Up to kGroup of a token's choices, the same in every lane.
+// Up to kGroup of a token's choices.
 struct Choices {
   int at[kGroup];      // row, or below 0 where nothing is to be touched
   bool live[kGroup];   // whether an expert has it
@@ -112,13 +119,33 @@ struct Piece {
   }
 };
 
-template <bool kBf16>
+// Threads that share a token, kWidth of them, a piece of its row each: a workgroup,
+// and gridDim.y of these, for long rows; a wave or 16 lanes for short ones, which
+// leave fewer idle (65536 rows of 32 bf16, combine and its gradient: 35 and 197 us by
+// workgroups, 8.1 and 15 by 16 lanes; 8192 x 8 rows of 1000, 125 pieces: 24.1 and 66 by
+// workgroups, 24.9 and 71 by waves).
+template <int kWidth>
+struct Lanes {
+  static constexpr int kTokens = kThreads / kWidth;   // of a workgroup
+  int64_t piece, first, step;   // the thread's piece, its first token, and how far the next is
+
+  __device__ __forceinline__ Lanes() {
+    int slot = threadIdx.x / kWidth;
+    if (kWidth >= 64) slot = __builtin_amdgcn_readfirstlane(slot);   // rows' numbers then come by scalar loads
+    piece = (int64_t)blockIdx.y * kWidth + threadIdx.x % kWidth;
+    first = (int64_t)blockIdx.x * kTokens + slot;
+    step = (int64_t)gridDim.x * kTokens;
+  }
+};
+
+template <bool kBf16, int kWidth>
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(const RowArgs p) {
   using P = Piece<kBf16>;
-  const int64_t i = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * P::kCount;
+  const Lanes<kWidth> l;
+  const int64_t i = l.piece * P::kCount;
   const int count = (int)min((int64_t)P::kCount, p.h - i);
   if (count <= 0) return;
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+  for (int64_t t = l.first; t < p.tokens; t += l.step) {
     P v;   // bits as they are: a copy keeps NaN's
     v.load(p.x, t * p.h + i, count);
     P none;
@@ -209,13 +236,14 @@ __global__ __launch_bounds__(kThreads) void dispatch_quant_kernel(const RowArgs 
   }
 }
 
-template <bool kBf16>
+template <bool kBf16, int kWidth>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const RowArgs p) {
   using P = Piece<kBf16>;
-  const int64_t i = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * P::kCount;
+  const Lanes<kWidth> l;
+  const int64_t i = l.piece * P::kCount;
   const int count = (int)min((int64_t)P::kCount, p.h - i);
   if (count <= 0) return;
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+  for (int64_t t = l.first; t < p.tokens; t += l.step) {
     float sum[P::kCount] = {};
     for (int j0 = 0; j0 < p.top_k; j0 += kGroup) {
       const Choices c = choices_of(p, t, j0);
@@ -241,19 +269,21 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const RowArgs p) {
   }
 }
 
-// A workgroup a token; its threads' partial dot products meet in LDS.
-template <bool kBf16>
+// kWidth threads go through a token's whole row; their partial dot products meet by
+// shuffles, and a workgroup's waves' in LDS.
+template <bool kBf16, int kWidth>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(const RowArgs p) {
   using P = Piece<kBf16>;
   __shared__ float partial[kThreads / 64][kGroup];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+  const Lanes<kWidth> l;
+  for (int64_t t = l.first; t < p.tokens; t += l.step) {
     for (int j0 = 0; j0 < p.top_k; j0 += kGroup) {
       const Choices c = choices_of(p, t, j0);
       float w[kGroup], dot[kGroup] = {};
 #pragma unroll
       for (int j = 0; j < kGroup; ++j) w[j] = c.live[j] ? weight_of(p, t * p.top_k + j0 + j) : 0.0f;
-      for (int64_t i = (int64_t)threadIdx.x * P::kCount; i < p.h; i += kThreads * P::kCount) {
+      for (int64_t i = l.piece * P::kCount; i < p.h; i += kWidth * P::kCount) {
         const int count = (int)min((int64_t)P::kCount, p.h - i);
         P d, v[kGroup];
         d.load(p.x, t * p.h + i, count);
@@ -284,23 +314,31 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(const RowArg
       }
       if (!p.scales) continue;
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
+      for (int j = 0; j < kGroup; ++j)
 #pragma unroll
-        for (int s = 32; s > 0; s /= 2) dot[j] += __shfl_xor(dot[j], s);
-        if (lane == 0) partial[wave][j] = dot[j];
+        for (int s = min(kWidth, 64) / 2; s > 0; s /= 2) dot[j] += __shfl_xor(dot[j], s);
+      const int j = threadIdx.x % kWidth;   // the choice that the thread writes
+      float sum = 0.0f;
+      if (kWidth > 64) {
+        if (lane == 0)
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g) partial[wave][g] = dot[g];
+        __syncthreads();
+        if (j < kGroup)
+#pragma unroll
+          for (int v = 0; v < kThreads / 64; ++v) sum += partial[v][j];
+        __syncthreads();   // before the next group's partials
+      } else {
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) sum = j == g ? dot[g] : sum;
       }
-      __syncthreads();
-      if ((int)threadIdx.x < kGroup && j0 + (int)threadIdx.x < p.top_k) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int v = 0; v < kThreads / 64; ++v) sum += partial[v][threadIdx.x];
-        const int64_t c = t * p.top_k + j0 + threadIdx.x;
+      if (j < kGroup && j0 + j < p.top_k) {
+        const int64_t c = t * p.top_k + j0 + j;
         if (p.w_bf16)
           ((uint16_t *)p.scales)[c] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
         else
           ((float *)p.scales)[c] = sum;
       }
-      __syncthreads();   // before the next group's partials
     }
   }
 }
@@ -329,15 +367,30 @@ int64_t groups_of(int64_t n, int64_t each) { return (n + each - 1) / each; }
 
 }  // namespace
 
+// A kernel by the width that a row of h takes: pieces a thread; `whole`: the threads
+// of a token go through its whole row.
+#define FP8BSQ_BY_WIDTH(KERNEL, BF, P, WHOLE)                                                          \
+  do {                                                                                                 \
+    const int64_t pieces = groups_of((P).h, (BF) ? 8 : 4);                                             \
+    const int width = pieces > 96 ? 256 : pieces > 32 ? 64 : 16;                                       \
+    const int64_t across = (WHOLE) || pieces == 0 ? 1 : groups_of(pieces, width);                      \
+    const dim3 grid(token_groups(groups_of((P).tokens, kThreads / width), across), (unsigned)across);  \
+    const dim3 block(kThreads);                                                                        \
+    if (width == 256)                                                                                  \
+      hipLaunchKernelGGL((KERNEL<BF, 256>), grid, block, 0, stream, P);                                \
+    else if (width == 64)                                                                              \
+      hipLaunchKernelGGL((KERNEL<BF, 64>), grid, block, 0, stream, P);                                 \
+    else                                                                                               \
+      hipLaunchKernelGGL((KERNEL<BF, 16>), grid, block, 0, stream, P);                                 \
+  } while (0)
+
 hipError_t launch_expert_dispatch(const void *x, bool bf16, const int32_t *rows, int64_t tokens, int64_t top_k,
                                   int64_t h, void *y, hipStream_t stream) {
   const RowArgs p = row_args(x, rows, nullptr, false, tokens, top_k, h, y);
-  const int64_t across = groups_of(h, kThreads * (bf16 ? 8 : 4));
-  const dim3 grid(token_groups(tokens, across), (unsigned)across), block(kThreads);
   if (bf16)
-    hipLaunchKernelGGL(dispatch_kernel<true>, grid, block, 0, stream, p);
+    FP8BSQ_BY_WIDTH(dispatch_kernel, true, p, false);
   else
-    hipLaunchKernelGGL(dispatch_kernel<false>, grid, block, 0, stream, p);
+    FP8BSQ_BY_WIDTH(dispatch_kernel, false, p, false);
   return hipGetLastError();
 }
 
@@ -368,12 +421,10 @@ hipError_t launch_expert_dispatch_quant(const void *x, bool bf16, bool ue8m0, co
 hipError_t launch_expert_combine(const void *y, bool bf16, const int32_t *rows, const void *weights, bool w_bf16,
                                  int64_t tokens, int64_t top_k, int64_t h, void *out, hipStream_t stream) {
   const RowArgs p = row_args(y, rows, weights, w_bf16, tokens, top_k, h, out);
-  const int64_t across = groups_of(h, kThreads * (bf16 ? 8 : 4));
-  const dim3 grid(token_groups(tokens, across), (unsigned)across), block(kThreads);
   if (bf16)
-    hipLaunchKernelGGL(combine_kernel<true>, grid, block, 0, stream, p);
+    FP8BSQ_BY_WIDTH(combine_kernel, true, p, false);
   else
-    hipLaunchKernelGGL(combine_kernel<false>, grid, block, 0, stream, p);
+    FP8BSQ_BY_WIDTH(combine_kernel, false, p, false);
   return hipGetLastError();
 }
 
@@ -383,12 +434,13 @@ hipError_t launch_expert_combine_backward(const void *dout, const void *y, bool 
   RowArgs p = row_args(dout, rows, weights, w_bf16, tokens, top_k, h, dy);
   p.y = y;
   p.scales = dweights;
-  const dim3 grid(token_groups(tokens, 1)), block(kThreads);
   if (bf16)
-    hipLaunchKernelGGL(combine_backward_kernel<true>, grid, block, 0, stream, p);
+    FP8BSQ_BY_WIDTH(combine_backward_kernel, true, p, true);
   else
-    hipLaunchKernelGGL(combine_backward_kernel<false>, grid, block, 0, stream, p);
+    FP8BSQ_BY_WIDTH(combine_backward_kernel, false, p, true);
   return hipGetLastError();
 }
+
+#undef FP8BSQ_BY_WIDTH
 
 }  // namespace fp8bsq

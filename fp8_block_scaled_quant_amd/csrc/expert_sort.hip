@@ -14,6 +14,12 @@
 // the number of such lanes below it, and the first of them moves the wave's
 // counter on.  Every count is a sum over a fixed set, so equal calls give equal
 // rows.  Up to kSingle choices one workgroup does it all, without the first kernel.
+//
+// Bound by the latency of its steps, not by its bytes.  Measured, of 256 experts, the
+// kernels: 8 choices 2.1 us; 65536 choices 2.8 and 7.1.  Whole calls: 64 choices 5.0 us
+// (the host's part; by counting over one wave 8.0), 4096 6.4, 65536 9.3, 2^20 21.
+// Smaller shares than kChunk choices cost more in counts to add up (2^18 choices: 15.7
+// us with 1024, 12.8 with 2048).
 #include "device_common.h"
 #include "expert_launch.h"
 
