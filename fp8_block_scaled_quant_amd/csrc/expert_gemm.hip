@@ -38,14 +38,15 @@ struct ProductArgs {
 // The experts' rows as the offsets give them, in order and inside the matrix
 // whatever the offsets hold, and their token tiles' numbers.
 struct Table {
-  int begin[kMaxExperts + 1];   // expert's first row; the last: where the rows behind begin
-  int first[kMaxExperts + 1];   // its first token tile; the last: their number
+  int *begin;   // [experts + 1] expert's first row; the last: where the rows behind begin
+  int *first;   // [experts + 1] its first token tile; the last: their number
 };
 
 // The 256-row kernel's tiles of up to 128 rows, an expert's last, are a list of
 // their own behind the others: they take half as long, and in one list some
 // workgroups would get more of the long ones than others.
-struct SplitTable : Table {
+struct SplitTable {
+  int begin[kMaxExperts + 1], first[kMaxExperts + 1];
   int half[kMaxExperts + 1];    // experts before with such a tile; the last: their number
 };
 
@@ -230,21 +231,22 @@ __device__ __forceinline__ f32x4 gated4(f32x4 g, f32x4 u) {
 //
 // Four compute waves, and movers that issue all global->LDS transfers into a ring
 // of kSlots blocks of 128, kSlots - 1 ahead, over the ends of tiles: a workgroup's
-// blocks are one sequence.  That keeps enough bytes in flight to stream weights
-// (16 KB a block) at HBM's rate, also where tiles are short.  One barrier a block
-// hands the ring on; a block's fragments are read to registers while the block
-// before it feeds the MFMAs.
+// blocks are one sequence.  One barrier a block hands the ring on.  Two workgroups a
+// CU fill each other's waits, and keep 64 and 96 KB of weights in flight together,
+// enough to stream them at HBM's rate (one workgroup with their LDS and fragments
+// read a block ahead: 64 experts of 2300 x 1408 with 64 rows each 49 us for 40, 16 of
+// 2 x 512 x 1024 with 8 rows 7.0 for 6.1, large weights the same).
 //
-// Measured: one token at eight experts of 2 x 2048 x 7168 43.5 us, 235 MB at 5.4 TB/s
+// Measured: one token at eight experts of 2 x 2048 x 7168 43.3 us, 235 MB at 5.4 TB/s
 // (a 1 GiB copy: 5.1; a wave per 16 features without LDS: 83 us); 8 rows each at 64
-// experts 316 us, 1.9 GB at 6.0 TB/s; 66 rows each, unevenly, at 64 of 2300 x 1408 59
-// us, 3.9 TB/s: experts above 64 rows take a second tile, whose weights L2 holds.
+// experts 318 us, 1.9 GB at 6.0 TB/s; 66 rows each, unevenly, at 64 of 2300 x 1408 58
+// us, 3.9 TB/s: experts above 64 rows take more tiles, 3.6 rounds of them.
 // ---------------------------------------------------------------------------
 constexpr int kStreamRows = 128;   // of weights, a tile
 
 template <int kTokens>
 struct StreamShape {
-  static constexpr int kSlots = kTokens == 64 ? 5 : 7;
+  static constexpr int kSlots = kTokens == 64 ? 3 : 4;     // two workgroups' in a CU's LDS
   static constexpr int kMovers = kTokens == 64 ? 2 : 4;    // of weights; one more of a
   static constexpr int kThreads = 64 * (4 + kMovers + 1);
   static constexpr int kAcross = kTokens == 64 ? 2 : 4;    // compute waves along the weights' rows
@@ -257,13 +259,15 @@ struct StreamShape {
 };
 
 template <bool kGated, int kTokens>
-__global__ __launch_bounds__(StreamShape<kTokens>::kThreads) void product_stream_kernel(const ProductArgs p) {
+__global__ __launch_bounds__(StreamShape<kTokens>::kThreads, kTokens == 64 ? 4 : 5) void product_stream_kernel(const ProductArgs p) {
   using S = StreamShape<kTokens>;
   constexpr int kFeatures = kGated ? kStreamRows / 2 : kStreamRows;
   constexpr int kWaveRows = kStreamRows / S::kAcross;   // of weights, a compute wave; gated: gate's, then up's
   constexpr int kAhead = S::kSlots - 1;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[S::kSlots * S::kSlotBytes];
-  __shared__ Table table;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t ring[];
+  Table table;
+  table.begin = (int *)(ring + S::kSlots * S::kSlotBytes);
+  table.first = table.begin + p.experts + 1;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fq = lane >> 4, dr = lane >> 3, ds = lane & 7;
@@ -366,7 +370,7 @@ __global__ __launch_bounds__(StreamShape<kTokens>::kThreads) void product_stream
     };
     // the block read next, and the tile being computed
     uint32_t turn = 0;
-    int kb = 0, slot = 0, done = 0;
+    int kb = 0, slot = 0;
     Tile ahead = tile_of(0), tile = ahead;
     auto read = [&](Block &v) __attribute__((always_inline)) {
       const uint8_t *a = ring + slot * S::kSlotBytes, *b = a + kTokens * kBlock;
@@ -428,32 +432,22 @@ __global__ __launch_bounds__(StreamShape<kTokens>::kThreads) void product_stream
         }
       }
     };
-    Block even, odd;
-    workgroup_barrier();
+    Block v;
     clear();
-    read(even);
-    auto step = [&](int64_t s, const Block &cur, Block &next) __attribute__((always_inline)) {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // block s's reads ended: its slot may be refilled
-      workgroup_barrier();                                 // s + 1 landed
-      const Tile then = ahead;
-      if (s + 1 < blocks) read(next);
-      __builtin_amdgcn_sched_barrier(0);
-      if (wa < tile.left) compute(cur);
-      __builtin_amdgcn_sched_barrier(0);
-      if (++done == nkb) {
+#pragma nounroll
+    for (int64_t s = 0; s < blocks; ++s) {
+      workgroup_barrier();   // block s landed
+      const bool last = kb + 1 == nkb;
+      read(v);
+      if (wa < tile.left) compute(v);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read: its slot may be refilled
+      if (last) {
         finish();
         clear();
-        done = 0;
-        tile = then;   // the next block's
+        tile = ahead;   // the next block's
       }
-    };
-    int64_t s = 0;
-#pragma nounroll
-    for (; s + 1 < blocks; s += 2) {
-      step(s, even, odd);
-      step(s + 1, odd, even);
     }
-    if (s < blocks) step(s, even, odd);
+    workgroup_barrier();   // the movers' last
   }
   clear_behind(p, table.begin[p.experts], 256);
 }
@@ -673,11 +667,13 @@ template <int kTokens>
 hipError_t launch_stream(ProductArgs p, bool gated, int cus, hipStream_t stream) {
   const int features = gated ? kStreamRows / 2 : kStreamRows;
   p.tiles_f = (int)((p.f + features - 1) / features);
-  const dim3 grid((unsigned)cus), block(StreamShape<kTokens>::kThreads);
+  using S = StreamShape<kTokens>;
+  const size_t lds = (size_t)S::kSlots * S::kSlotBytes + 2 * (size_t)(p.experts + 1) * sizeof(int);
+  const dim3 grid((unsigned)(2 * cus)), block(S::kThreads);
   if (gated)
-    hipLaunchKernelGGL((product_stream_kernel<true, kTokens>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((product_stream_kernel<true, kTokens>), grid, block, lds, stream, p);
   else
-    hipLaunchKernelGGL((product_stream_kernel<false, kTokens>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((product_stream_kernel<false, kTokens>), grid, block, lds, stream, p);
   return hipGetLastError();
 }
 
@@ -703,25 +699,32 @@ hipError_t launch_big(ProductArgs p, bool gated, int cus, hipStream_t stream) {
 enum class Shape { kFew, kSome, kMany };
 
 // By the rows an expert has on average, which is all that the host knows.  Up to
-// eight, nearly no expert has more than 16 (us, tiles of 16 and 64 rows: 64 experts of
-// 2 x 2048 x 7168 with 4 rows each 294 and 299, 12 rows 312 and 314; 8 experts 36.0
-// and 36.9, 12 rows 50 and 38).  From there on the cheaper of 64 and 256 rows by the
-// time of a round of tiles on all CUs, so much per block of 128 and so much besides,
-// or by the weights' bytes; a partial tile an expert is half of one more on average.
-// Measured (64 and 256 rows): 64 experts of 2 x 2048 x 7168 with 64 rows 429 and 484,
-// 128 rows 637 and 507; of 2300 x 1408 with 64 rows 50 and 63, 128 rows 79 and 70;
-// 16 of 2 x 512 x 1024 with 128 rows 13.0 and 17.4, 384 rows 22.1 and 18.2.
+// eight, nearly no expert has more than 16 (us, tiles of 16 and 64 rows: 16 experts of
+// 2 x 512 x 1024 6.1 and 7.4, 8 of 2 x 2048 x 7168 34.8 and 35.8).  From there on the
+// cheaper of 64 and 256 rows: rounds of tiles on all CUs, each so much per block of 128
+// and so much besides, and the weights' bytes, of which some three tenths of the
+// shorter show beside the longer.  A partial tile an expert is half of one more on
+// average; two tiles of 64 rows share a CU; short tiles of the 256-row kernel, up to
+// some 128 rows an expert, cost less and fill up its later rounds.  Measured (64 and 256
+// rows): 8 experts of 2 x 2048 x 7168 with 96 rows 48 and 75; 64 of 2300 x 1408 with 96
+// rows 47 and 64; 64 of 2 x 2048 x 7168 with 64 rows 445 and 484, with 80 rows 503 and
+// 469; 128 of 2 x 768 x 2048 with 64 rows 94 and 109, with 160 rows 148 and 124.
 Shape product_shape(int64_t rows, int64_t experts, int64_t f, int64_t k, bool gated, int cus) {
   const double active = (double)min(rows, experts), each = (double)rows / active, nkb = (double)(k / kBlock);
   if (each <= 8) return Shape::kFew;
   auto rounds = [&](double rows_a_tile, double features) {
     const double tokens = each / rows_a_tile + 0.5;
-    return ceil(active * (tokens > 1.0 ? tokens : 1.0) * ceil((double)f / features) / cus);
+    return active * (tokens > 1.0 ? tokens : 1.0) * ceil((double)f / features) / cus;
   };
   const double weights_us = active * (double)f * (double)k * (gated ? 2.0 : 1.0) / 5.1e6;
-  const double some_us = rounds(64, gated ? 64 : 128) * (nkb * 0.48 + 1.7);
-  const double many_us = rounds(256, gated ? 128 : 256) * (nkb * (each <= 128 ? 1.2 : 1.8) + 7.0);
-  return many_us < some_us && weights_us < some_us ? Shape::kMany : Shape::kSome;
+  auto with_weights = [&](double us) {
+    return us < weights_us ? weights_us + 0.3 * us : us + 0.3 * weights_us;
+  };
+  const double some = ceil(rounds(64, gated ? 64 : 128)), pairs = floor(some / 2);
+  const double some_us = pairs * (nkb * 0.87 + 0.8) + (some - 2 * pairs) * (nkb * 0.5 + 0.8);
+  const double many = rounds(256, gated ? 128 : 256), full = each <= 64 ? 0.0 : each >= 192 ? 1.0 : (each - 64) / 128;
+  const double many_us = (many <= 3 ? ceil(many) : many + 0.5) * (nkb * (1.2 + 0.4 * full) + 5.0);
+  return with_weights(many_us) < with_weights(some_us) ? Shape::kMany : Shape::kSome;
 }
 
 }  // namespace
