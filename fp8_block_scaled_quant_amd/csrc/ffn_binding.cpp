@@ -240,9 +240,11 @@ Tensor clip(const py::list &grads, const std::optional<py::list> &outs, double m
 // Experts
 // ---------------------------------------------------------------------------
 
-// A contiguous tensor of its own over part of a 1-D one's storage.
-Tensor piece(const Tensor &all, int64_t offset, at::IntArrayRef shape) {
-  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+// A contiguous tensor of its own over part of another's storage, from its
+// `offset`-th element on.
+Tensor piece(const Tensor &all, int64_t offset, at::IntArrayRef shape, at::ScalarType dtype) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                      c10::scalarTypeToTypeMeta(dtype));
   t.unsafeGetTensorImpl()->set_storage_offset(offset);
   t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
   return t;
@@ -259,8 +261,9 @@ py::tuple expert_sort(const Tensor &experts, int64_t num_experts) {
   const c10::DeviceGuard guard(device);
   // one allocation for the three: the call is shorter than two more
   const Tensor all = empty({num_experts + 1 + 2 * n}, at::kInt, device);
-  const Tensor offsets = piece(all, 0, {num_experts + 1}), rows = piece(all, num_experts + 1, experts.sizes()),
-               choices = piece(all, num_experts + 1 + n, {n});
+  const Tensor offsets = piece(all, 0, {num_experts + 1}, at::kInt),
+               rows = piece(all, num_experts + 1, experts.sizes(), at::kInt),
+               choices = piece(all, num_experts + 1 + n, {n}, at::kInt);
   const size_t bytes = fp8bsq_expert_sort_workspace(n, num_experts);
   Tensor ws;
   if (bytes) ws = workspace(bytes, device);
@@ -333,7 +336,15 @@ py::tuple expert_dispatch_quant(const Tensor &x, const Tensor &rows, int scale_f
   const int64_t h = x.size(-1), n = c.tokens * c.top_k;
   if (h % 128 != 0) value("H must be a multiple of 128");
   const c10::DeviceGuard guard(device);
-  const Tensor y = empty({n, h}, at::kFloat8_e4m3fn, device), s = empty({n, h / 128}, at::kFloat, device);
+  Tensor y, s;
+  if (n * h <= 1 << 20) {   // a decode step's, which is shorter than a second allocation
+    const Tensor all = empty({n * h + n * (h / 128) * 4}, at::kByte, device);
+    y = piece(all, 0, {n, h}, at::kFloat8_e4m3fn);
+    s = piece(all, n * h / 4, {n, h / 128}, at::kFloat);
+  } else {
+    y = empty({n, h}, at::kFloat8_e4m3fn, device);
+    s = empty({n, h / 128}, at::kFloat, device);
+  }
   check_status(fp8_expert_dispatch_quant(x.data_ptr(), dtype, scale_fmt, c.rows, c.tokens, c.top_k, h,
                                          (uint8_t *)y.data_ptr(), (float *)s.data_ptr(), stream_of(device)));
   return py::make_tuple(y, s);
