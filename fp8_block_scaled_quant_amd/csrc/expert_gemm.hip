@@ -32,7 +32,7 @@ struct ProductArgs {
   int64_t rows, f, k;
   int experts, nkb;
   int tiles_f, blocks_f;    // tiles and 128-wide blocks of the features
-  bool out_bf16, vec, vec8;   // four outputs of a row make one aligned store; eight bf16 ones do
+  bool out_bf16;
 };
 
 // The experts' rows as the offsets give them, in order and inside the matrix
@@ -192,31 +192,49 @@ __device__ __forceinline__ void clear_behind(const ProductArgs &p, int behind, i
   for (int64_t i = self; i < (end - inner_end) / 2; i += all) ((uint16_t *)inner_end)[i] = 0;
 }
 
-// Four consecutive outputs of a row.
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_at2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// Four consecutive outputs of a row, which may start on any element; one by one
+// where they pass its end.
 __device__ __forceinline__ void store_four(const ProductArgs &p, int64_t row, int64_t col, f32x4 v) {
   const int64_t at = row * p.f + col;
-  const int left = (int)min((int64_t)4, p.f - col);
-  if (p.out_bf16) {
-    if (p.vec) store4<true, true>(p.out, at, v, 4); else store4<true, false>(p.out, at, v, left);
-  } else {
-    if (p.vec) store4<false, true>(p.out, at, v, 4); else store4<false, false>(p.out, at, v, left);
+  if (col + 4 <= p.f) {
+    if (p.out_bf16)
+      *(u32x2_at2 *)((uint16_t *)p.out + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    else
+      *(f32x4_at4 *)((float *)p.out + at) = v;
+    return;
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (col + e < p.f) store_out(p.out, p.out_bf16, at + e, v[e]);
 }
 
-// A row's outputs in two neighbouring 16-wide tiles, `col` the first's first: eight
-// consecutive bf16 a lane instead of four in each tile, so that a store covers 64
-// bytes of a row.  The swap leaves tile 0's columns in the even groups of 16 lanes
-// and tile 1's in the odd ones.
+// A row's outputs in two neighbouring 16-wide tiles, `col` the first's first.  bf16:
+// eight consecutive ones a lane instead of four in each tile, so that a store covers
+// 64 bytes of a row.  The swap leaves tile 0's columns in the even groups of 16 lanes
+// and tile 1's in the odd ones.  (5300 rows of 6746, on any 2 bytes: 47 us, 98 with
+// stores of one element.)
 __device__ __forceinline__ void store_pair(const ProductArgs &p, bool there, int64_t row, int64_t col, int fq, f32x4 v0, f32x4 v1) {
-  if (!p.vec8) {
+  if (!p.out_bf16) {
     if (there && col + 4 * fq < p.f) store_four(p, row, col + 4 * fq, v0);
     if (there && col + 16 + 4 * fq < p.f) store_four(p, row, col + 16 + 4 * fq, v1);
     return;
   }
   const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v0[0], v0[1]), pack_bf16x2(v1[0], v1[1]), false, false);
   const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v0[2], v0[3]), pack_bf16x2(v1[2], v1[3]), false, false);
-  const int64_t at = col + 16 * (fq & 1) + 8 * (fq >> 1);
-  if (there && at < p.f) *(u32x4 *)((uint16_t *)p.out + row * p.f + at) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+  const u32x4 v = {lo[0], hi[0], lo[1], hi[1]};
+  const int64_t first = col + 16 * (fq & 1) + 8 * (fq >> 1);
+  uint16_t *to = (uint16_t *)p.out + row * p.f + first;
+  if (there && first + 8 <= p.f) {
+    *(u32x4_at2 *)to = v;
+  } else if (there) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (first + e < p.f) to[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+  }
 }
 
 __device__ __forceinline__ f32x4 gated4(f32x4 g, f32x4 u) {
@@ -748,8 +766,6 @@ hipError_t launch_expert_product(const uint8_t *a, const float *a_s, const int32
   p.nkb = (int)(k / kBlock);
   p.blocks_f = (int)((f + kBlock - 1) / kBlock);
   p.out_bf16 = out_bf16;
-  p.vec8 = out_bf16 && f % 8 == 0 && ((uintptr_t)out & 15) == 0;
-  p.vec = f % 4 == 0 && ((uintptr_t)out & (out_bf16 ? 7 : 15)) == 0;
   int cus = current_device_cus();
   if (cus <= 0) cus = 256;
   const bool gated = w1 != nullptr;
