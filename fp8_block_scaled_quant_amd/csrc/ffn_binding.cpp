@@ -258,6 +258,7 @@ py::tuple expert_sort(const Tensor &experts, int64_t num_experts) {
   if (experts.dim() == 0) value("expert numbers must be [..., top_k]");
   if (num_experts <= 0) value("num_experts must be positive");
   const int64_t n = experts.numel();
+  if (num_experts > 1024 || n >= (int64_t)1 << 31) check_status(FP8BSQ_ERANGE);   // before memory for them is asked for
   const c10::DeviceGuard guard(device);
   // one allocation for the three: the call is shorter than two more
   const Tensor all = empty({num_experts + 1 + 2 * n}, at::kInt, device);

@@ -13,7 +13,7 @@ from typing import NamedTuple
 import torch
 
 from . import _DTYPE, _ffn_lib, act_quant, weight_quant
-from .ffn import _format, _out
+from .ffn import _format, _operand, _out
 
 
 class ExpertSort(NamedTuple):
@@ -97,7 +97,8 @@ def expert_dispatch(x: torch.Tensor, rows: torch.Tensor) -> torch.Tensor:
 
 def expert_dispatch_quant(x: torch.Tensor, rows: torch.Tensor, scale_fmt=None):
     """``act_quant(expert_dispatch(x, rows), 128, scale_fmt)``, each token quantized
-    once: ``y`` (float8_e4m3fn [n, H]) and ``s`` (float32 [n, H / 128])."""
+    once: ``y`` (float8_e4m3fn [n, H]) and ``s`` (float32 [n, H / 128]).  Autograd does
+    not see this call, nor the products'."""
     return _ffn_lib.ext().expert_dispatch_quant(x, rows, _format(scale_fmt))
 
 
@@ -190,7 +191,7 @@ class Experts(torch.nn.Module):
         """``x`` [..., K]; ``experts`` and ``weights`` [..., top_k], a router's choices."""
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
-        x = x.to(self.dtype).contiguous()
+        x = _operand(x.to(self.dtype))
         offsets, rows, _ = expert_sort(experts.contiguous(), self.num_experts)
         a, a_s = expert_dispatch_quant(x, rows, self.scale_fmt)
         h = expert_gated_ffn(a, a_s, offsets, self.w_gate, self.w_gate_scale, self.w_up, self.w_up_scale, self.dtype)

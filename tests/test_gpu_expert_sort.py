@@ -78,8 +78,9 @@ def test_refusals():
             bad()
     with pytest.raises(TypeError):
         fb.expert_sort(ids.short(), 4)
-    with pytest.raises(fb.Fp8Error):
-        fb.expert_sort(ids, 1025)
+    for experts in (1025, 1 << 40, (1 << 63) - 1):   # refused, not allocated for
+        with pytest.raises(fb.Fp8Error):
+            fb.expert_sort(ids, experts)
 
 
 @pytest.mark.parametrize("tokens", [1, 300, 3000])

@@ -95,6 +95,16 @@ def test_tokens_are_independent():
     assert torch.equal(all_together, alone)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_rows_that_start_anywhere(kind):
+    """A contiguous view that is not 16-byte aligned: the same output."""
+    layer = _layer(3, 4, 128, 256, kind, None)
+    x, w = E.normal(1, (7, 128), kind).to(G.device()), torch.rand(7, 2, device=G.device())
+    ids = U.gpu(E.choices(2, 7, 2, 4))
+    shifted = lambda t: torch.cat([t.new_zeros(1), t.flatten()])[1:].view(t.shape)  # noqa: E731
+    assert shifted(x).data_ptr() % 16 and torch.equal(layer(shifted(x), shifted(ids), shifted(w)), layer(x, ids, w))
+
+
 def test_no_tokens_and_refusals():
     layer = _layer(1, 3, 128, 128, "bf16", None)
     x, ids, w = torch.zeros(0, 128, dtype=torch.bfloat16, device=G.device()), torch.zeros(0, 2, dtype=torch.int64, device=G.device()), torch.zeros(0, 2, device=G.device())
