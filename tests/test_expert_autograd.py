@@ -86,11 +86,10 @@ def test_second_order_exists_without_weights_alone(rows):
 
 def test_gradients_reach_what_comes_before_and_no_more(rows):
     x, scale = _leaf(TOKENS, H), _leaf(TOKENS, TOP_K)
-    w = torch.softmax(scale, 1)
-    out = fb.expert_combine(torch.tanh(fb.expert_dispatch(x, rows)), rows, w)
+    out = fb.expert_combine(torch.tanh(fb.expert_dispatch(x, rows)), rows, torch.softmax(scale, 1))
     gx, gs = torch.autograd.grad(out.square().sum(), (x, scale))
     live = (rows >= 0)[..., None]
-    dense = (torch.where(live, torch.tanh(x)[:, None].expand(-1, TOP_K, -1), 0.0) * w[..., None]).sum(1)
+    dense = (torch.where(live, torch.tanh(x)[:, None].expand(-1, TOP_K, -1), 0.0) * torch.softmax(scale, 1)[..., None]).sum(1)
     for got, want in zip((gx, gs), torch.autograd.grad(dense.square().sum(), (x, scale))):
         assert torch.allclose(got, want, rtol=1e-12, atol=1e-12)
     with torch.no_grad():
