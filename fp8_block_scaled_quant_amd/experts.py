@@ -130,7 +130,7 @@ def expert_gemm(a: torch.Tensor, a_s: torch.Tensor, offsets: torch.Tensor, b: to
 
     ``a`` [n, K] E4M3 with ``a_s`` [n, K/128]; ``b`` [E, N, K] E4M3 with ``b_s``
     [E, ceil(N/128), K/128]: ``fp8_gemm`` of every expert, in one call.  Returns
-    [n, N]; the rows behind are zero.
+    [n, N]; the rows behind are zero.  At most 65535 * 16 rows.
     """
     return _ffn_lib.ext().expert_gemm(a, a_s, offsets, b, b_s, _out(out_dtype))
 
@@ -147,6 +147,8 @@ class Experts(torch.nn.Module):
     """``out[t] = sum_j weights[t, j] * (silu(x W_gate^T) * (x W_up^T)) W_down^T`` with
     the weights of the experts that ``experts[t]`` names, held as E4M3 codes and
     128 x 128 block scales.
+
+    A call takes up to 65535 * 16 choices, the products' rows.
 
     Parameters (frozen; this is an inference layer): ``w_gate``, ``w_up`` [E, F, K] and
     ``w_down`` [E, K, F] float8_e4m3fn, with their ``.._scale``.  ``scale_fmt`` is the

@@ -204,7 +204,7 @@ FP8BSQ_API int fp8bsq_expert_dispatch(const void *x, int dtype, const int32_t *r
  * fp8_expert_dispatch_quant -- fp8_act_quant of that, each token quantized once.
  *
  *   x        [tokens, h], dtype x_dtype, 16-byte aligned; h % 128 == 0 (else
- *            FP8BSQ_ESHAPE).
+ *            FP8BSQ_ESHAPE), 0 <= h <= 2^21.
  *   y, s     [n, h] E4M3 codes out, 16-byte aligned, and [n, h / 128] FP32 scales
  *            out, 4-byte aligned; the rows behind are those of rows of zeros.
  */
@@ -229,7 +229,8 @@ FP8BSQ_API int fp8bsq_expert_combine(const void *y, int dtype, const int32_t *ro
  *     dy[rows[t, j]] = weights[t, j] dout[t]             (rows behind: zero)
  *     dweights[t, j] = sum of dout[t] * y[rows[t, j]]    (taking no part: zero)
  *
- *   dout     [tokens, h], y [n, h], dy [n, h] out, of `dtype`.
+ *   dout     [tokens, h], y [n, h], dy [n, h] out, of `dtype`; 0 <= h <= 2^21.  All are
+ *            aligned to their elements, and dy overlaps no other tensor.
  *   dy       or NULL: not computed.
  *   dweights [tokens, top_k] out, dtype w_dtype, or NULL: not computed (y is not
  *            read and may then be NULL).  Sums are FP32, in a fixed order.
