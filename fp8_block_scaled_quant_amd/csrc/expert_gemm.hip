@@ -8,9 +8,10 @@
 // the launch depends on sizes only.  Within an expert the tiles of one piece of
 // weight follow each other, so that it comes from HBM once.
 //
-// Two kernels: tiles of 16 or 64 rows by 128 rows of weights, with transfers many
-// blocks ahead, for few rows an expert (bound by the weights' bytes), and of 256 by
-// 256, for many (bound by the matrix cores).
+// Three kernels: tiles of 16 or 64 rows by 128 rows of weights, with transfers many
+// blocks ahead, for few rows an expert (bound by the weights' bytes); of 256 by 256,
+// for many (bound by the matrix cores); and of 16 by 32 or 64, four K blocks at a
+// time, where these are no more than the CUs (bound by the chain along K).
 #include "device_cus.h"
 #include "e4m3_tiles.h"
 #include "expert_launch.h"
@@ -471,6 +472,198 @@ __global__ __launch_bounds__(StreamShape<kTokens>::kThreads, kTokens == 64 ? 4 :
 }
 
 // ---------------------------------------------------------------------------
+// Few tiles: 16 rows by 32 or 64 rows of weights (gated: of gate's and up's, half
+// each), a workgroup a CU.
+//
+// With one tile a workgroup the time is a chain along K, and a CU takes data that is in
+// no cache at some 55 GB/s at best.  So small tiles spread the weights over the CUs, and
+// a step of the chain is four K blocks, one to each compute wave.  The waves' sums meet
+// in LDS, always in the same order.  Four movers load a block of the step's weights
+// each and a fifth a's, two steps ahead (32 rows: four), over the ends of tiles.
+//
+// Measured, weights from HBM (us; the kernel above): one row at each of 8 experts of
+// 2 x 256 x 7168 11.0 (22.6; with 64 rows a tile 14.7), of 2 x 512 x 7168 14.4 (24.0),
+// of 2 x 1024 x 7168 23.8, 64 rows a tile (27.3); one of 4096 x 4096 7.4 (11.2); 16 rows
+// at each of 8 of 2 x 256 x 7168 12.4 (29.9), 128 rows at one of 2 x 512 x 7168 9.5 (25.6).
+// ---------------------------------------------------------------------------
+constexpr int kLongTokens = 16, kLongParts = 4, kLongThreads = 64 * (2 * kLongParts + 1);
+
+template <int kRows>   // of weights, a tile
+struct LongShape {
+  static constexpr int kSlots = kRows == 64 ? 3 : 5;
+  static constexpr int kJ = kRows / 16;   // MFMA tiles of a block
+  static constexpr int kPartBytes = (kLongTokens + kRows) * kBlock + 64 * 4;
+  static constexpr int kStepBytes = kLongParts * kPartBytes;
+  static constexpr int kJoinBytes = kLongParts * kJ * 64 * (int)sizeof(f32x4);
+  static constexpr int kDmaA = kLongParts * (kLongTokens / 8 + 1), kDmaB = kRows / 8;   // transfers a step and mover
+  static_assert((kSlots - 1) * (kDmaA > kDmaB ? kDmaA : kDmaB) < 64, "the wait counter's range");
+};
+
+template <bool kGated, int kRows>
+__global__ __launch_bounds__(kLongThreads) void product_long_kernel(const ProductArgs p) {
+  using S = LongShape<kRows>;
+  constexpr int kFeatures = kGated ? kRows / 2 : kRows;
+  constexpr int kAhead = S::kSlots - 1;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t ring[];
+  f32x4 *join = (f32x4 *)(ring + S::kSlots * S::kStepBytes);   // [part][16 rows of weights][lane]
+  Table table;
+  table.begin = (int *)(ring + S::kSlots * S::kStepBytes + S::kJoinBytes);
+  table.first = table.begin + p.experts + 1;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fr = lane & 15, fq = lane >> 4, dr = lane >> 3, ds = lane & 7;
+  build_table<kLongThreads, kLongTokens>(p, table);
+  const uint32_t ntiles = (uint32_t)__builtin_amdgcn_readfirstlane(table.first[p.experts]) * (uint32_t)p.tiles_f;
+  const int nkb = p.nkb, steps = (nkb + kLongParts - 1) / kLongParts;
+  const uint32_t mine = blockIdx.x < ntiles ? (ntiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+  const int64_t all = (int64_t)mine * steps;
+  auto tile_of = [&](uint32_t i) { return locate<kLongTokens, kFeatures>(p, table, blockIdx.x + i * gridDim.x, ntiles, lane); };
+
+  if (wave >= kLongParts) {
+    if (all == 0) return;
+    uint32_t turn = 0;
+    int step = 0, slot = 0;
+    // past the end the last step again, and past K its last block, so that every
+    // step counts the same
+    auto drive = [&](auto enter, auto issue, auto wait_landed) __attribute__((always_inline)) {
+#pragma unroll 1
+      for (int64_t s = 0; s < all + kAhead; ++s) {
+        if (step == 0) enter(tile_of(turn));
+        issue(step * kLongParts, lds_addr(ring) + (uint32_t)slot * S::kStepBytes);   // into the slot of step s - S::kSlots, whose reads ended before the last barrier
+        slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+        if (step + 1 < steps) {
+          ++step;
+        } else if (turn + 1 < mine) {
+          ++turn;
+          step = 0;
+        }
+        if (s >= kAhead - 1) {
+          wait_landed();   // all but the youngest kAhead - 1 steps
+          workgroup_barrier();
+        }
+      }
+      wait_dma_all();   // transfers past the end, before the workgroup's LDS is released
+    };
+    if (wave == kLongParts) {
+      uint32_t off[kLongTokens / 8], s_off = 0;
+      const uint8_t *base = nullptr;
+      const float *scales = nullptr;
+      drive(
+          [&](const Tile &t) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kLongTokens / 8; ++i) {
+              const int row = 8 * i + dr;
+              off[i] = (uint32_t)min(row, t.left - 1) * (uint32_t)p.k + ((ds ^ swz(row)) << 4);
+            }
+            s_off = (uint32_t)min(lane, t.left - 1) * (uint32_t)nkb * 4;
+            base = p.a + (int64_t)t.row0 * p.k;
+            scales = p.a_s + (int64_t)t.row0 * nkb;
+          },
+          [&](int kb0, uint32_t to) __attribute__((always_inline)) {
+#pragma unroll
+            for (int q = 0; q < kLongParts; ++q) {
+              const int64_t kb = min(kb0 + q, nkb - 1);
+#pragma unroll
+              for (int i = 0; i < kLongTokens / 8; ++i) lds_dma16(base + kb * kBlock, off[i], to + q * S::kPartBytes + i * 1024);
+              lds_dma4(scales + kb, s_off, to + q * S::kPartBytes + (kLongTokens + kRows) * kBlock);
+            }
+          },
+          [&]() __attribute__((always_inline)) { asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * S::kDmaA) : "memory"); });
+    } else {
+      const int part = wave - kLongParts - 1;
+      uint32_t off[kRows / 8];
+      const uint8_t *base0 = nullptr, *base1 = nullptr;
+      drive(
+          [&](const Tile &t) __attribute__((always_inline)) {
+            const int left = (int)min((int64_t)kFeatures, p.f - t.f0);
+#pragma unroll
+            for (int i = 0; i < kRows / 8; ++i) {
+              const int row = 8 * i + dr;
+              off[i] = (uint32_t)min(row % kFeatures, left - 1) * (uint32_t)p.k + ((ds ^ swz(row)) << 4);
+            }
+            const int64_t at = ((int64_t)t.expert * p.f + t.f0) * p.k;
+            base0 = p.w0 + at;
+            base1 = kGated ? p.w1 + at : base0;
+          },
+          [&](int kb0, uint32_t to) __attribute__((always_inline)) {
+            const int64_t kb = min(kb0 + part, nkb - 1);
+#pragma unroll
+            for (int i = 0; i < kRows / 8; ++i)
+              lds_dma16((8 * i < kFeatures ? base0 : base1) + kb * kBlock, off[i],
+                        to + part * S::kPartBytes + kLongTokens * kBlock + i * 1024);
+          },
+          [&]() __attribute__((always_inline)) { asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * S::kDmaB) : "memory"); });
+    }
+    return;
+  }
+
+  if (all > 0) {
+    uint32_t turn = 0;
+    int step = 0, slot = 0;
+    bool joined = false;   // a tile's sums are in LDS, from before the last barrier
+    Tile tile = tile_of(0), done = tile;
+    f32x4 acc[S::kJ];
+#pragma unroll
+    for (int j = 0; j < S::kJ; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto sum = [&](int j) {
+      f32x4 v = join[j * 64 + lane];
+#pragma unroll
+      for (int q = 1; q < kLongParts; ++q) v += join[(q * S::kJ + j) * 64 + lane];
+      return v;
+    };
+    auto finish = [&]() __attribute__((always_inline)) {   // 16 features a wave
+      const int64_t col = done.f0 + 16 * wave + 4 * fq;
+      if (16 * wave >= kFeatures || fr >= done.left || col >= p.f) return;
+      store_four(p, done.row0 + fr, col, kGated ? gated4(sum(wave), sum(wave + S::kJ / 2)) : sum(wave));
+    };
+#pragma nounroll
+    for (int64_t s = 0; s < all; ++s) {
+      workgroup_barrier();   // step s landed
+      const int kb = step * kLongParts + wave;
+      if (kb < nkb) {
+        const uint8_t *a = ring + slot * S::kStepBytes + wave * S::kPartBytes, *b = a + kLongTokens * kBlock;
+        const int64_t at = ((int64_t)tile.expert * p.blocks_f + tile.f0 / kBlock) * nkb + kb;
+        const float w0 = load_uniform(p.w0_s, at), w1 = kGated ? load_uniform(p.w1_s, at) : w0;
+        const float sa = ((const float *)(b + kRows * kBlock))[fr];
+        const i32x8 av = frag_from_lds(a + fr * kBlock, fq, fr);
+        i32x8 bv[S::kJ];
+#pragma unroll
+        for (int j = 0; j < S::kJ; ++j) bv[j] = frag_from_lds(b + (16 * j + fr) * kBlock, fq, 16 * j + fr);
+        f32x4 prt[S::kJ];
+#pragma unroll
+        for (int j = 0; j < S::kJ; ++j) prt[j] = mfma_e4m3_16x16x128(bv[j], av, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int j = 0; j < S::kJ; ++j) {
+          const float sc = sa * (kGated && j >= S::kJ / 2 ? w1 : w0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] = __builtin_fmaf(prt[j][e], sc, acc[j][e]);
+        }
+      }
+      slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+      if (joined) finish();
+      joined = false;
+      if (++step == steps) {
+        // a tile has two steps at least (product_shape): the last tile's sums were
+        // read before the barrier that began this step
+#pragma unroll
+        for (int j = 0; j < S::kJ; ++j) {
+          join[(wave * S::kJ + j) * 64 + lane] = acc[j];
+          acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        joined = true;
+        done = tile;
+        step = 0;
+        if (++turn < mine) tile = tile_of(turn);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read, and its sums written: its slot may be refilled
+    }
+    workgroup_barrier();   // the movers' last
+    finish();
+  }
+  clear_behind(p, table.begin[p.experts], 64 * kLongParts);
+}
+
+// ---------------------------------------------------------------------------
 // Many rows an expert: 256 rows by 256 rows of weights (gated: 128 features' gate
 // and up).
 //
@@ -695,6 +888,20 @@ hipError_t launch_stream(ProductArgs p, bool gated, int cus, hipStream_t stream)
   return hipGetLastError();
 }
 
+template <int kRows>
+hipError_t launch_long(ProductArgs p, bool gated, int cus, hipStream_t stream) {
+  using S = LongShape<kRows>;
+  const int features = gated ? kRows / 2 : kRows;
+  p.tiles_f = (int)((p.f + features - 1) / features);
+  const size_t lds = (size_t)S::kSlots * S::kStepBytes + S::kJoinBytes + 2 * (size_t)(p.experts + 1) * sizeof(int);
+  const dim3 grid((unsigned)cus), block(kLongThreads);
+  if (gated)
+    hipLaunchKernelGGL((product_long_kernel<true, kRows>), grid, block, lds, stream, p);
+  else
+    hipLaunchKernelGGL((product_long_kernel<false, kRows>), grid, block, lds, stream, p);
+  return hipGetLastError();
+}
+
 hipError_t launch_big(ProductArgs p, bool gated, int cus, hipStream_t stream) {
   const int features = gated ? kBigTile / 2 : kBigTile;
   p.tiles_f = (int)((p.f + features - 1) / features);
@@ -714,10 +921,16 @@ hipError_t launch_big(ProductArgs p, bool gated, int cus, hipStream_t stream) {
   return hipGetLastError();
 }
 
-enum class Shape { kFew, kSome, kMany };
+enum class Shape { kLong32, kLong64, kFew, kSome, kMany };
 
-// By the rows an expert has on average, which is all that the host knows.  Up to
-// eight, nearly no expert has more than 16 (us, tiles of 16 and 64 rows: 16 experts of
+// By the rows an expert has on average, which is all that the host knows; an expert's
+// last tile counts as half a one.  Where tiles of 16 by 32 or 64 fit one round of the
+// CUs they win, if the chain along K is long enough for steps of four blocks (us, 128
+// rows of weights a tile, 32 and 64: 8 experts of 1024 x 640 with a row 5.7, 5.5 and
+// 5.8; 16 of 2 x 512 x 1024 with 8 rows, 256 tiles of 64, 6.8 and 7.2; with a row of 2 x
+// 512 x 1536 9.2 and 8.8); beyond a round they do not (8 of 2 x 1280 x 7168, 320 tiles
+// of 64: 29.6 and 33.2).  Else, up to
+// eight rows, nearly no expert has more than 16 (us, tiles of 16 and 64 rows: 16 experts of
 // 2 x 512 x 1024 6.1 and 7.4, 8 of 2 x 2048 x 7168 34.8 and 35.8).  From there on the
 // cheaper of 64 and 256 rows: rounds of tiles on all CUs, each so much per block of 128
 // and so much besides, and the weights' bytes, of which some three tenths of the
@@ -729,6 +942,12 @@ enum class Shape { kFew, kSome, kMany };
 // 469; 128 of 2 x 768 x 2048 with 64 rows 94 and 109, with 160 rows 148 and 124.
 Shape product_shape(int64_t rows, int64_t experts, int64_t f, int64_t k, bool gated, int cus) {
   const double active = (double)min(rows, experts), each = (double)rows / active, nkb = (double)(k / kBlock);
+  auto tiles = [&](int weight_rows) {   // of 16 rows
+    const double tokens = each / kLongTokens + 0.5, features = gated ? weight_rows / 2 : weight_rows;
+    return active * (tokens > 1.0 ? tokens : 1.0) * ceil((double)f / features);
+  };
+  if (nkb > kLongParts && tiles(32) <= cus) return Shape::kLong32;
+  if (nkb >= 12 && tiles(64) <= cus) return Shape::kLong64;
   if (each <= 8) return Shape::kFew;
   auto rounds = [&](double rows_a_tile, double features) {
     const double tokens = each / rows_a_tile + 0.5;
@@ -770,6 +989,8 @@ hipError_t launch_expert_product(const uint8_t *a, const float *a_s, const int32
   if (cus <= 0) cus = 256;
   const bool gated = w1 != nullptr;
   switch (product_shape(rows, experts, f, k, gated, cus)) {
+    case Shape::kLong32: return launch_long<32>(p, gated, cus, stream);
+    case Shape::kLong64: return launch_long<64>(p, gated, cus, stream);
     case Shape::kFew: return launch_stream<16>(p, gated, cus, stream);
     case Shape::kSome: return launch_stream<64>(p, gated, cus, stream);
     default: return launch_big(p, gated, cus, stream);
