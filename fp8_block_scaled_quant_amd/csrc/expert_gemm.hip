@@ -929,10 +929,9 @@ enum class Shape { kLong32, kLong64, kFew, kSome, kMany };
 // rows of weights a tile, 32 and 64: 8 experts of 1024 x 640 with a row 5.7, 5.5 and
 // 5.8; 16 of 2 x 512 x 1024 with 8 rows, 256 tiles of 64, 6.8 and 7.2; with a row of 2 x
 // 512 x 1536 9.2 and 8.8); beyond a round they do not (8 of 2 x 1280 x 7168, 320 tiles
-// of 64: 29.6 and 33.2).  Else, up to
-// eight rows, nearly no expert has more than 16 (us, tiles of 16 and 64 rows: 16 experts of
-// 2 x 512 x 1024 6.1 and 7.4, 8 of 2 x 2048 x 7168 34.8 and 35.8).  From there on the
-// cheaper of 64 and 256 rows: rounds of tiles on all CUs, each so much per block of 128
+// of 64: 29.6 and 33.2).  Else, up to eight rows, nearly no expert has more than 16 (us,
+// tiles of 16 and 64 rows: 16 experts of 2 x 512 x 1024 6.1 and 7.4, 8 of 2 x 2048 x
+// 7168 34.8 and 35.8).  From there on the cheaper of 64 and 256 rows: rounds of tiles on all CUs, each so much per block of 128
 // and so much besides, and the weights' bytes, of which some three tenths of the
 // shorter show beside the longer.  A partial tile an expert is half of one more on
 // average; two tiles of 64 rows share a CU; short tiles of the 256-row kernel, up to
