@@ -165,9 +165,14 @@ __global__ __launch_bounds__(64 * kMaxWaves) void sort_place_kernel(const SortAr
       const uint32_t row = first[b] + next + below;
       p.rows[c] = (int32_t)(b < p.num ? row : ~row);
       p.choices[row] = (int32_t)c;
-      // after every lane's read above: a wave's LDS accesses are executed in order
+      // Lanes of one bucket read the counter, and one of them writes it.  The hardware
+      // executes a wave's LDS accesses in order; the fences, no instructions themselves,
+      // hold the compiler to it: the write stays behind these reads, and the next
+      // round's reads behind the write.
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       if (below == 0) mine[b] = next + (uint32_t)__popcll(same);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
 #pragma unroll
   for (int r = 0; r < kHeld; ++r)
