@@ -41,6 +41,7 @@ HIP_FLAGS = [
     "-fvisibility=hidden",
     "-ffp-contract=off",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    "-DFP8BSQ_ALL_LAUNCHERS",   # the ABI layers refer to every launcher, and a library without one does not link
     "-Wno-unused-command-line-argument",
 ]
 
@@ -68,9 +69,7 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
     objs = {src: os.path.join(objdir, src + ".o") for src in SOURCES + FFN_SOURCES}
     # the slowest source first, so that the others compile beside it
     for src in sorted(objs, key=lambda s: s != "block_gemm.hip"):
-        lang = ["-x", "hip"] if src.endswith(".hip") else []
-        cmd = [cc, *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, *lang, "-c",
-               os.path.join(CSRC, src), "-o", objs[src]]
+        cmd = _compile_command(cc, src, objs[src])
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
@@ -78,9 +77,9 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
             _drain(procs[:1])
             procs = procs[1:]
     _drain(procs)
-    _link(cc, [objs[s] for s in SOURCES], [], LIB_PATH, verbose)
+    _link(cc, [objs[s] for s in SOURCES], ["-Wl,--no-undefined"], LIB_PATH, verbose)
     # found beside it at run time
-    _link(cc, [objs[s] for s in FFN_SOURCES], ["-L", PKG_DIR, "-lfp8bsq", "-Wl,-rpath,$ORIGIN"], FFN_LIB_PATH, verbose)
+    _link(cc, [objs[s] for s in FFN_SOURCES], _ffn_link(), FFN_LIB_PATH, verbose)
     if missing:
         print(f"{missing} not found: the Python binding, {os.path.basename(BINDING_PATH)}, is not built", file=sys.stderr)
         return LIB_PATH
@@ -91,6 +90,15 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
           ["-L", PKG_DIR, "-lfp8bsq_ffn", "-Wl,-rpath,$ORIGIN", *dirs, "-ltorch_python", "-ltorch_cpu", "-lc10",
            "-lc10_hip"], BINDING_PATH, verbose)
     return LIB_PATH
+
+
+def _compile_command(cc, src, obj):
+    lang = ["-x", "hip"] if src.endswith(".hip") else []
+    return [cc, *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+
+
+def _ffn_link():
+    return ["-Wl,--no-undefined", "-L", PKG_DIR, "-lfp8bsq", "-Wl,-rpath,$ORIGIN"]
 
 
 def _binding_command(objdir, verbose):

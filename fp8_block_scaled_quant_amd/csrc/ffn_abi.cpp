@@ -9,8 +9,10 @@
 #include "ffn_launch.h"
 #include "fp8bsq_ffn.h"
 
+#ifndef FP8BSQ_ALL_LAUNCHERS
 namespace fp8bsq {
-// Weak, so that this layer can be built over the other launchers alone.
+// Weak, so that this layer can be built over the other launchers' stand-ins alone.
+// The library's own build defines the macro: there each launcher has to be linked.
 __attribute__((weak)) decltype(expert_sort_bytes) expert_sort_bytes;
 __attribute__((weak)) decltype(launch_expert_sort) launch_expert_sort;
 __attribute__((weak)) decltype(launch_expert_dispatch) launch_expert_dispatch;
@@ -19,6 +21,7 @@ __attribute__((weak)) decltype(launch_expert_combine) launch_expert_combine;
 __attribute__((weak)) decltype(launch_expert_combine_backward) launch_expert_combine_backward;
 __attribute__((weak)) decltype(launch_expert_product) launch_expert_product;
 }  // namespace fp8bsq
+#endif
 
 namespace {
 
