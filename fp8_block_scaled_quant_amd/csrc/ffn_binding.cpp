@@ -250,6 +250,18 @@ Tensor piece(const Tensor &all, int64_t offset, at::IntArrayRef shape, at::Scala
   return t;
 }
 
+// The library's ranges (fp8bsq_ffn.h), so that a size beyond them is refused before
+// memory for its outputs is asked for.
+constexpr int64_t kMaxExperts = 1024, kMaxChoices = (int64_t)1 << 31, kMaxFeatures = (int64_t)1 << 21;
+constexpr int64_t kMaxProductRows = (int64_t)65535 * 16;
+
+void require_range(bool ok) {
+  if (!ok) check_status(FP8BSQ_ERANGE);
+}
+
+// n sorted rows of h; none of them, or none of a length, are within every range.
+void require_rows(int64_t n, int64_t h) { require_range(n == 0 || h == 0 || (n < kMaxChoices && h <= kMaxFeatures)); }
+
 py::tuple expert_sort(const Tensor &experts, int64_t num_experts) {
   const c10::Device device = experts.device();
   require_gpu(experts, device);
@@ -258,7 +270,7 @@ py::tuple expert_sort(const Tensor &experts, int64_t num_experts) {
   if (experts.dim() == 0) value("expert numbers must be [..., top_k]");
   if (num_experts <= 0) value("num_experts must be positive");
   const int64_t n = experts.numel();
-  if (num_experts > 1024 || n >= (int64_t)1 << 31) check_status(FP8BSQ_ERANGE);   // before memory for them is asked for
+  require_range(num_experts <= kMaxExperts && n < kMaxChoices);
   const c10::DeviceGuard guard(device);
   // one allocation for the three: the call is shorter than two more
   const Tensor all = empty({num_experts + 1 + 2 * n}, at::kInt, device);
@@ -320,9 +332,10 @@ py::object expert_dispatch(const Tensor &x, const Tensor &rows, bool ask) {
   if (dtype < 0) type("expert_dispatch takes bf16 or fp32 rows");
   const Choices c = choices_of(rows);
   require_tokens(x, rows);
-  const int64_t h = x.size(-1);
+  const int64_t h = x.size(-1), n = c.tokens * c.top_k;
+  require_rows(n, h);
   const c10::DeviceGuard guard(device);
-  const Tensor y = empty({c.tokens * c.top_k, h}, x.scalar_type(), device);
+  const Tensor y = empty({n, h}, x.scalar_type(), device);
   check_status(fp8bsq_expert_dispatch(x.data_ptr(), dtype, c.rows, c.tokens, c.top_k, h, y.data_ptr(), stream_of(device)));
   return py::cast(y);
 }
@@ -336,6 +349,7 @@ py::tuple expert_dispatch_quant(const Tensor &x, const Tensor &rows, int scale_f
   require_tokens(x, rows);
   const int64_t h = x.size(-1), n = c.tokens * c.top_k;
   if (h % 128 != 0) value("H must be a multiple of 128");
+  require_rows(n, h);
   const c10::DeviceGuard guard(device);
   Tensor y, s;
   if (n * h <= 1 << 20) {   // a decode step's, which is shorter than a second allocation
@@ -361,6 +375,7 @@ py::object expert_combine(const Tensor &y, const Tensor &rows, const std::option
   require_sorted(y, c);
   const int w_dtype = require_weights(weights, rows, device);
   const int64_t h = y.size(1);
+  require_rows(y.size(0), h);
   const c10::DeviceGuard guard(device);
   const Tensor out = empty(with_last(rows, h), y.scalar_type(), device);
   check_status(fp8bsq_expert_combine(y.data_ptr(), dtype, c.rows, data_or_null(weights), w_dtype, c.tokens, c.top_k, h,
@@ -380,6 +395,7 @@ py::tuple expert_combine_backward(const Tensor &dout, const Tensor &y, const Ten
   if (y.size(1) != dout.size(-1)) value("dout and y must have rows of one length");
   const int w_dtype = require_weights(weights, rows, device);
   const int64_t h = y.size(1);
+  require_rows(y.size(0), h);
   const c10::DeviceGuard guard(device);
   Tensor dy, dw;
   if (row_grad) dy = empty(y.sizes(), y.scalar_type(), device);
@@ -418,6 +434,8 @@ Tensor expert_product(const Tensor &a, const Tensor &a_s, const Tensor &offsets,
   const Weight second = w1 ? expert_weight(*w1, *w1_s, w0.sizes()) : Weight{nullptr, nullptr};
   if (offsets.scalar_type() != at::kInt) type("offsets must be int32, as expert_sort returns them");
   if (offsets.dim() != 1 || offsets.size(0) != experts + 1) value("offsets must be [E + 1]");
+  // nothing to do is within every range
+  require_range(rows == 0 || f == 0 || (rows <= kMaxProductRows && experts <= kMaxExperts && f <= kMaxFeatures && k <= kMaxFeatures));
   const c10::DeviceGuard guard(device);
   const Tensor out = empty({rows, f}, scalar_type(out_dtype), device);
   const uint8_t *codes = (const uint8_t *)a.data_ptr();
