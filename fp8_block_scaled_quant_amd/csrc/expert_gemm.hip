@@ -902,11 +902,14 @@ hipError_t launch_long(ProductArgs p, bool gated, int cus, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Whether the scales of a row's four blocks are a 16-byte transfer's.
+bool scales_by_four(int nkb, const float *a_s) { return nkb % 4 == 0 && ((uintptr_t)a_s & 15) == 0; }
+
 hipError_t launch_big(ProductArgs p, bool gated, int cus, hipStream_t stream) {
   const int features = gated ? kBigTile / 2 : kBigTile;
   p.tiles_f = (int)((p.f + features - 1) / features);
   const dim3 grid((unsigned)cus), block(kBigThreads);
-  const bool quad = p.nkb % 4 == 0 && ((uintptr_t)p.a_s & 15) == 0;
+  const bool quad = scales_by_four(p.nkb, p.a_s);
   if (gated) {
     if (quad)
       hipLaunchKernelGGL((product_big_kernel<true, true>), grid, block, 0, stream, p);
