@@ -12,6 +12,7 @@ import pytest
 from tests import test_gpu_expert_shapes as shapes
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CUS = 256
 
 
 @pytest.fixture(scope="module")
@@ -38,6 +39,18 @@ def kernels(tmp_path_factory):
 
 def test_sizes_take_the_kernels_they_are_there_for(kernels):
     assert kernels(shapes.CASES) == list(shapes.SIZES.values())
-    # every kernel for more than a few tiles
+    # every kernel that there is
     assert {(shape, case[0]) for case, shape in shapes.SIZES.items()} == \
-        {(shape, gated) for shape in ("many by four", "many", "some", "few") for gated in (False, True)}
+        {(shape, gated) for shape in ("many by four", "many", "some", "few", "long32", "long64") for gated in (False, True)}
+
+
+def test_few_tiles_are_more_than_the_workgroups():
+    """... of each kind, with two steps of four K blocks a tile and with more."""
+    steps = {}
+    for (gated, counts, _, n, k), shape in shapes.SIZES.items():
+        if shape.startswith("long"):
+            features = int(shape[4:]) // (2 if gated else 1)
+            assert sum(-(-c // 16) for c in counts) * -(-n // features) > CUS
+            steps.setdefault((shape, gated), set()).add(-(-k // 512))
+    assert len(steps) == 4 and all(min(s) == 2 and max(s) > 2 for (shape, _), s in steps.items() if shape == "long32")
+    assert all(min(s) == 3 and max(s) > 3 for (shape, _), s in steps.items() if shape == "long64")   # from 12 blocks on

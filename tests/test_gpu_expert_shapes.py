@@ -36,6 +36,15 @@ SIZES = {
     (True, SOME, 5, 701, 384): "some",
     (False, FEW, 5, 1300, 640): "few",
     (True, FEW, 5, 1301, 256): "few",
+    # and of these the tiles are more than 256, so that workgroups go on to a second: two steps of K blocks each, or more
+    (False, (17, 1), 0, 3840, 640): "long32",
+    (False, (33, 1, 1, 1), 0, 1901, 1152): "long32",
+    (True, (17, 1), 0, 1904, 640): "long32",
+    (True, (57, 1, 1, 1, 1, 1, 1, 1), 0, 497, 1152): "long32",
+    (False, (33, 1, 1, 1), 0, 3839, 1536): "long64",
+    (False, (57, 1, 1, 1, 1, 1, 1, 1), 0, 1920, 1664): "long64",
+    (True, (17, 1), 0, 3839, 1536): "long64",
+    (True, (17, 1, 17, 1), 0, 1900, 2176): "long64",
 }
 CASES = list(SIZES)
 
@@ -102,7 +111,7 @@ def test_scales_that_start_anywhere(case):
 
 
 ONE_EACH = [next(c for c in CASES if SIZES[c] == shape and c[0] == gated)
-            for shape in ("many by four", "many", "some", "few") for gated in (False, True)]
+            for shape in ("many by four", "many", "some", "few", "long32", "long64") for gated in (False, True)]
 
 
 @pytest.mark.parametrize("case", ONE_EACH, ids=_name)
