@@ -1,6 +1,6 @@
 """Every kernel of the experts' products, each at sizes that choose it
-(test_expert_plans.py asks the rule itself): values, output types, writes, replays,
-threads.  Bounds as in test_gpu_expert_products.
+(test_expert_plans.py asks the rule itself): values, output types, writes, offsets of
+any contents, replays, threads.  Bounds as in test_gpu_expert_products.
 """
 
 import functools
@@ -108,6 +108,38 @@ def test_scales_that_start_anywhere(case):
     want = _call(case, args)
     args[1] = torch.cat([args[1].new_zeros(1), args[1].flatten()])[1:].view(args[1].shape)
     assert args[1].data_ptr() % 16 and torch.equal(_call(case, args), want)
+
+
+def _disorders(experts, rows):
+    rng = np.random.default_rng(experts)
+    yield np.full(experts + 1, 2 ** 31 - 1)
+    yield np.full(experts + 1, -2 ** 31)
+    yield np.full(experts + 1, rows // 2)
+    yield np.arange(experts + 1)[::-1] * 7 - 5
+    yield np.arange(experts + 1) % 2 * rows
+    yield np.r_[rows // 3, rng.integers(-rows, 2 * rows, experts)]
+    yield np.sort(rng.integers(0, rows + 1, experts + 1))
+
+
+@pytest.mark.parametrize("case", CASES, ids=_name)
+def test_offsets_of_any_contents(case):
+    """Offsets that expert_sort does not write touch nothing outside.  What they give is
+    unspecified for a caller; the kernels take the largest so far, within the rows, and a
+    mistake there shows in the values."""
+    _, counts, behind, n, _ = case
+    rows, args = sum(counts) + behind, _device(case)
+    args[0][rows - behind:] = 0x38   # 1.0, and 1: with other offsets these rows are some expert's
+    args[1][rows - behind:] = 1
+    for bad in _disorders(len(counts), rows):
+        G.announce(f"{_name(case)}, offsets {bad[:4]} ..")
+        order = np.maximum.accumulate(np.clip(bad, 0, rows)).astype(np.int32)
+        got, guard = U.guarded_like((rows, n), torch.bfloat16)
+        args[2] = U.gpu(bad.astype(np.int32))
+        _into(case, args, got, _lib.BF16)
+        guard.check_guards()
+        args[2] = U.gpu(order)
+        assert torch.equal(got[order[0]:], _call(case, args)[order[0]:])
+        assert not got[order[-1]:].any()
 
 
 ONE_EACH = [next(c for c in CASES if SIZES[c] == shape and c[0] == gated)
