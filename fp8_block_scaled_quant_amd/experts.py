@@ -131,6 +131,9 @@ def expert_gemm(a: torch.Tensor, a_s: torch.Tensor, offsets: torch.Tensor, b: to
     ``a`` [n, K] E4M3 with ``a_s`` [n, K/128]; ``b`` [E, N, K] E4M3 with ``b_s``
     [E, ceil(N/128), K/128]: ``fp8_gemm`` of every expert, in one call.  Returns
     [n, N]; the rows behind are zero.  At most 65535 * 16 rows.
+
+    Equal calls give equal bits.  From K = 640 on, a row's last bits can change with the
+    number of rows that come along (another kernel adds the K blocks in another order).
     """
     return _ffn_lib.ext().expert_gemm(a, a_s, offsets, b, b_s, _out(out_dtype))
 
@@ -148,7 +151,9 @@ class Experts(torch.nn.Module):
     the weights of the experts that ``experts[t]`` names, held as E4M3 codes and
     128 x 128 block scales.
 
-    A call takes up to 65535 * 16 choices, the products' rows.
+    A call takes up to 65535 * 16 choices, the products' rows.  A token's output does not
+    depend on which tokens come with it; with K or F of 640 and more its last bits can
+    depend on how many do, as ``expert_gemm``'s.
 
     Parameters (frozen; this is an inference layer): ``w_gate``, ``w_up`` [E, F, K] and
     ``w_down`` [E, K, F] float8_e4m3fn, with their ``.._scale``.  ``scale_fmt`` is the

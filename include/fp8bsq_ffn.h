@@ -253,7 +253,10 @@ FP8BSQ_API int fp8bsq_expert_combine_backward(const void *dout, const void *y, i
  *            FP8BSQ_EINVAL); rows <= 65535 * 16, n, k <= 2^21, num_experts as above
  *            (else FP8BSQ_ERANGE).  rows or n = 0: nothing to do.
  *
- * Results meet fp8_block_gemm's error bound.
+ * Results meet fp8_block_gemm's error bound.  Equal calls give equal bits.  The order in
+ * which a row's K blocks are added goes by rows, num_experts, n and k: up to k = 512 it
+ * is always the same, and from k = 640 on a row's last bits can change with the number
+ * of rows that come along.
  */
 FP8BSQ_API int fp8_expert_gemm(const uint8_t *a, const float *a_s, const int32_t *offsets, const uint8_t *b,
                     const float *b_s, void *c, int c_dtype, int64_t rows, int64_t num_experts, int64_t n, int64_t k,
