@@ -37,10 +37,16 @@ struct ProductArgs {
 };
 
 // The experts' rows as the offsets give them, in order and inside the matrix
-// whatever the offsets hold, and their token tiles' numbers.
+// whatever the offsets hold, and their token tiles' numbers.  These fit 16 bits: the
+// rows make at most 65535 * 16 / 64 tiles of 64, and an expert one more; tiles of 16
+// are taken up to eight rows an expert or some hundred tiles (product_shape).
 struct Table {
-  int *begin;   // [experts + 1] expert's first row; the last: where the rows behind begin
-  int *first;   // [experts + 1] its first token tile; the last: their number
+  int *begin;        // [experts + 1] expert's first row; the last: where the rows behind begin
+  uint16_t *first;   // [experts + 1] its first token tile; the last: their number
+
+  __device__ __forceinline__ Table(uint8_t *at, int experts)
+      : begin((int *)at), first((uint16_t *)(begin + experts + 1)) {}
+  static constexpr size_t bytes(int64_t experts) { return (size_t)(experts + 1) * sizeof(int) + (size_t)(experts + 2) / 2 * 4; }
 };
 
 // The 256-row kernel's tiles of up to 128 rows, an expert's last, are a list of
@@ -133,6 +139,18 @@ __device__ __forceinline__ int expert_of(const int *prefix, int experts, uint32_
   int e = 0;
   for (int e0 = 1; e0 <= experts; e0 += 64)
     e += __popcll(__ballot(e0 + lane <= experts && (uint32_t)prefix[min(e0 + lane, experts)] <= q));
+  return __builtin_amdgcn_readfirstlane(e);
+}
+
+// Two entries a lane; entry 0, which is 0, always counts.
+__device__ __forceinline__ int expert_of(const uint16_t *prefix, int experts, uint32_t q, int lane) {
+  typedef uint32_t __attribute__((may_alias)) Pair;
+  int e = -1;
+  for (int e0 = 0; e0 <= experts; e0 += 128) {
+    const int i = e0 + 2 * lane;
+    const uint32_t two = ((const Pair *)prefix)[min(i, experts) / 2];
+    e += __popcll(__ballot(i <= experts && (two & 0xFFFFu) <= q)) + __popcll(__ballot(i < experts && two >> 16 <= q));
+  }
   return __builtin_amdgcn_readfirstlane(e);
 }
 
@@ -254,7 +272,10 @@ __device__ __forceinline__ f32x4 gated4(f32x4 g, f32x4 u) {
 // CU fill each other's waits, and keep 64 and 96 KB of weights in flight together,
 // enough to stream them at HBM's rate (one workgroup with their LDS and fragments
 // read a block ahead: 64 experts of 2300 x 1408 with 64 rows each 49 us for 40, 16 of
-// 2 x 512 x 1024 with 8 rows 7.0 for 6.1, large weights the same).
+// 2 x 512 x 1024 with 8 rows 7.0 for 6.1, large weights the same).  So that they fit
+// with 1024 experts too, the tables hold tile numbers of 16 bits and the ring starts on
+// 128 bytes: 1024 experts of 2 x 512 x 1024 with 8 rows 117 us, 189 with one workgroup a
+// CU; 2 x 256 x 1024 with 48 rows 84 and 123.
 //
 // Measured: one token at eight experts of 2 x 2048 x 7168 43.3 us, 235 MB at 5.4 TB/s
 // (a 1 GiB copy: 5.1; a wave per 16 features without LDS: 83 us); 8 rows each at 64
@@ -262,6 +283,7 @@ __device__ __forceinline__ f32x4 gated4(f32x4 g, f32x4 u) {
 // us, 3.9 TB/s: experts above 64 rows take more tiles, 3.6 rounds of them.
 // ---------------------------------------------------------------------------
 constexpr int kStreamRows = 128;   // of weights, a tile
+constexpr int kRingAlign = 128;    // whole rows; both kernels' rings are one symbol, and so of one alignment
 
 template <int kTokens>
 struct StreamShape {
@@ -275,6 +297,12 @@ struct StreamShape {
   static constexpr int kSlotBytes = (kTokens + kStreamRows) * kBlock + kScales * 4;
   static constexpr int kDmaA = kTokens / 8 + 1, kDmaB = 16 / kMovers;   // transfers a block and mover
   static_assert((kSlots - 1) * (kDmaA > kDmaB ? kDmaA : kDmaB) < 64, "the wait counter's range");
+
+  // of LDS that a launch asks for; the scan's, a place for each wave and three sums, is
+  // the kernel's own
+  static constexpr size_t lds(int64_t experts) { return (size_t)kSlots * kSlotBytes + Table::bytes(experts); }
+  static_assert(3 * (kThreads / 64) * sizeof(int) <= kRingAlign && kSlotBytes % kRingAlign == 0 &&
+                    2 * (lds(kMaxExperts) + kRingAlign) <= 160 * 1024, "two workgroups a CU");
 };
 
 template <bool kGated, int kTokens>
@@ -283,10 +311,8 @@ __global__ __launch_bounds__(StreamShape<kTokens>::kThreads, kTokens == 64 ? 4 :
   constexpr int kFeatures = kGated ? kStreamRows / 2 : kStreamRows;
   constexpr int kWaveRows = kStreamRows / S::kAcross;   // of weights, a compute wave; gated: gate's, then up's
   constexpr int kAhead = S::kSlots - 1;
-  extern __shared__ __attribute__((aligned(1024))) uint8_t ring[];
-  Table table;
-  table.begin = (int *)(ring + S::kSlots * S::kSlotBytes);
-  table.first = table.begin + p.experts + 1;
+  extern __shared__ __attribute__((aligned(kRingAlign))) uint8_t ring[];
+  Table table(ring + S::kSlots * S::kSlotBytes, p.experts);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fq = lane >> 4, dr = lane >> 3, ds = lane & 7;
@@ -504,11 +530,9 @@ __global__ __launch_bounds__(kLongThreads) void product_long_kernel(const Produc
   using S = LongShape<kRows>;
   constexpr int kFeatures = kGated ? kRows / 2 : kRows;
   constexpr int kAhead = S::kSlots - 1;
-  extern __shared__ __attribute__((aligned(1024))) uint8_t ring[];
+  extern __shared__ __attribute__((aligned(kRingAlign))) uint8_t ring[];
   f32x4 *join = (f32x4 *)(ring + S::kSlots * S::kStepBytes);   // [part][16 rows of weights][lane]
-  Table table;
-  table.begin = (int *)(ring + S::kSlots * S::kStepBytes + S::kJoinBytes);
-  table.first = table.begin + p.experts + 1;
+  Table table(ring + S::kSlots * S::kStepBytes + S::kJoinBytes, p.experts);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fq = lane >> 4, dr = lane >> 3, ds = lane & 7;
@@ -879,7 +903,7 @@ hipError_t launch_stream(ProductArgs p, bool gated, int cus, hipStream_t stream)
   const int features = gated ? kStreamRows / 2 : kStreamRows;
   p.tiles_f = (int)((p.f + features - 1) / features);
   using S = StreamShape<kTokens>;
-  const size_t lds = (size_t)S::kSlots * S::kSlotBytes + 2 * (size_t)(p.experts + 1) * sizeof(int);
+  const size_t lds = S::lds(p.experts);
   const dim3 grid((unsigned)(2 * cus)), block(S::kThreads);
   if (gated)
     hipLaunchKernelGGL((product_stream_kernel<true, kTokens>), grid, block, lds, stream, p);
@@ -893,7 +917,7 @@ hipError_t launch_long(ProductArgs p, bool gated, int cus, hipStream_t stream) {
   using S = LongShape<kRows>;
   const int features = gated ? kRows / 2 : kRows;
   p.tiles_f = (int)((p.f + features - 1) / features);
-  const size_t lds = (size_t)S::kSlots * S::kStepBytes + S::kJoinBytes + 2 * (size_t)(p.experts + 1) * sizeof(int);
+  const size_t lds = (size_t)S::kSlots * S::kStepBytes + S::kJoinBytes + Table::bytes(p.experts);
   const dim3 grid((unsigned)cus), block(kLongThreads);
   if (gated)
     hipLaunchKernelGGL((product_long_kernel<true, kRows>), grid, block, lds, stream, p);
