@@ -274,8 +274,9 @@ __device__ __forceinline__ f32x4 gated4(f32x4 g, f32x4 u) {
 // read a block ahead: 64 experts of 2300 x 1408 with 64 rows each 49 us for 40, 16 of
 // 2 x 512 x 1024 with 8 rows 7.0 for 6.1, large weights the same).  So that they fit
 // with 1024 experts too, the tables hold tile numbers of 16 bits and the ring starts on
-// 128 bytes: 1024 experts of 2 x 512 x 1024 with 8 rows 117 us, 189 with one workgroup a
-// CU; 2 x 256 x 1024 with 48 rows 84 and 123.
+// 128 bytes (1024 experts, two workgroups a CU and one: 64 rows each of 2 x 512 x 512
+// 137 and 182 us, 48 of 2 x 256 x 1024 127 and 147, 8 of 2 x 512 x 1024 193 and 209; one
+// row of 128 x 256, weights in the cache, 12 and 21).
 //
 // Measured: one token at eight experts of 2 x 2048 x 7168 43.3 us, 235 MB at 5.4 TB/s
 // (a 1 GiB copy: 5.1; a wave per 16 features without LDS: 83 us); 8 rows each at 64
@@ -505,7 +506,8 @@ __global__ __launch_bounds__(StreamShape<kTokens>::kThreads, kTokens == 64 ? 4 :
 // no cache at some 55 GB/s at best.  So small tiles spread the weights over the CUs, and
 // a step of the chain is four K blocks, one to each compute wave.  The waves' sums meet
 // in LDS, always in the same order.  Four movers load a block of the step's weights
-// each and a fifth a's, two steps ahead (32 rows: four), over the ends of tiles.
+// each and a fifth a's, two steps ahead (32 rows: four), over the ends of tiles.  They
+// go as the movers above do, and a fix to one loop belongs in both.
 //
 // Measured, weights from HBM (us; the kernel above): one row at each of 8 experts of
 // 2 x 256 x 7168 11.0 (22.6; with 64 rows a tile 14.7), of 2 x 512 x 7168 14.4 (24.0),
@@ -951,7 +953,9 @@ hipError_t launch_big(ProductArgs p, bool gated, int cus, hipStream_t stream) {
 enum class Shape { kLong32, kLong64, kFew, kSome, kMany };
 
 // By the rows an expert has on average, which is all that the host knows; an expert's
-// last tile counts as half a one.  Where tiles of 16 by 32 or 64 fit one round of the
+// last tile counts as half a one.  Choices that take no part count as rows: where seven
+// of eight are at other ranks' experts, 256 tokens' 8 choices at 32 experts of 2 x 2048 x
+// 7168 take 192 us, and 157 with those rows alone that are here.  Where tiles of 16 by 32 or 64 fit one round of the
 // CUs they win, if the chain along K is long enough for steps of four blocks (us, 128
 // rows of weights a tile, 32 and 64: 8 experts of 1024 x 640 with a row 5.7, 5.5 and
 // 5.8; 16 of 2 x 512 x 1024 with 8 rows, 256 tiles of 64, 6.8 and 7.2; with a row of 2 x

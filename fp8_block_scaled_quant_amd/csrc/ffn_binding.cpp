@@ -272,7 +272,8 @@ py::tuple expert_sort(const Tensor &experts, int64_t num_experts) {
   const int64_t n = experts.numel();
   require_range(num_experts <= kMaxExperts && n < kMaxChoices);
   const c10::DeviceGuard guard(device);
-  // one allocation for the three: the call is shorter than two more
+  // one allocation for the three, which any of them keeps in use: one token's call is
+  // bound by the host (4.8 us, with three allocations 5.4)
   const Tensor all = empty({num_experts + 1 + 2 * n}, at::kInt, device);
   const Tensor offsets = piece(all, 0, {num_experts + 1}, at::kInt),
                rows = piece(all, num_experts + 1, experts.sizes(), at::kInt),
@@ -352,7 +353,10 @@ py::tuple expert_dispatch_quant(const Tensor &x, const Tensor &rows, int scale_f
   require_rows(n, h);
   const c10::DeviceGuard guard(device);
   Tensor y, s;
-  if (n * h <= 1 << 20) {   // a decode step's, which is shorter than a second allocation
+  // A decode step's call is bound by the host, and a second allocation shows in it (us a
+  // call, ue8m0, 18 and 19 tokens' 8 choices of 7168, either side of the bound: 3.8 and
+  // 4.2).  Larger outputs have their own, so that one can be freed without the other.
+  if (n * h <= 1 << 20) {
     const Tensor all = empty({n * h + n * (h / 128) * 4}, at::kByte, device);
     y = piece(all, 0, {n, h}, at::kFloat8_e4m3fn);
     s = piece(all, n * h / 4, {n, h / 128}, at::kFloat);
