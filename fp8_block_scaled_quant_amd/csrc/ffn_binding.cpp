@@ -6,6 +6,7 @@
 //
 // Wrong types raise TypeError, wrong shapes or devices ValueError, and a status
 // of the library its Fp8Error.
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
@@ -240,14 +241,23 @@ Tensor clip(const py::list &grads, const std::optional<py::list> &outs, double m
 // Experts
 // ---------------------------------------------------------------------------
 
-// A contiguous tensor of its own over part of another's storage, from its
-// `offset`-th element on.
-Tensor piece(const Tensor &all, int64_t offset, at::IntArrayRef shape, at::ScalarType dtype) {
+// A contiguous int32 tensor of its own over part of another's storage, from its
+// `offset`-th element on.  Of one type with it: torch does not save tensors that share
+// a storage and differ in type.
+Tensor piece(const Tensor &all, int64_t offset, at::IntArrayRef shape) {
   Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
-                                                      c10::scalarTypeToTypeMeta(dtype));
+                                                      c10::scalarTypeToTypeMeta(at::kInt));
   t.unsafeGetTensorImpl()->set_storage_offset(offset);
   t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
   return t;
+}
+
+// A tensor from the allocator of a call's first output, but not through torch's
+// dispatcher, which a decode step's call, bound by the host, would feel a second time
+// (16 tokens' 8 choices of 7168, quantized: 4.2 us a call for 4.5).
+Tensor beside(const Tensor &first, at::IntArrayRef shape, at::ScalarType dtype) {
+  return at::detail::empty_generic(shape, first.storage().allocator(), c10::DispatchKeySet(c10::DispatchKey::CUDA), dtype,
+                                   std::nullopt);
 }
 
 // The library's ranges (fp8bsq_ffn.h), so that a size beyond them is refused before
@@ -273,11 +283,11 @@ py::tuple expert_sort(const Tensor &experts, int64_t num_experts) {
   require_range(num_experts <= kMaxExperts && n < kMaxChoices);
   const c10::DeviceGuard guard(device);
   // one allocation for the three, which any of them keeps in use: one token's call is
-  // bound by the host (4.8 us, with three allocations 5.4)
+  // bound by the host (4.0 us; with three allocations 4.5, through the dispatcher 5.0)
   const Tensor all = empty({num_experts + 1 + 2 * n}, at::kInt, device);
-  const Tensor offsets = piece(all, 0, {num_experts + 1}, at::kInt),
-               rows = piece(all, num_experts + 1, experts.sizes(), at::kInt),
-               choices = piece(all, num_experts + 1 + n, {n}, at::kInt);
+  const Tensor offsets = piece(all, 0, {num_experts + 1}),
+               rows = piece(all, num_experts + 1, experts.sizes()),
+               choices = piece(all, num_experts + 1 + n, {n});
   const size_t bytes = fp8bsq_expert_sort_workspace(n, num_experts);
   Tensor ws;
   if (bytes) ws = workspace(bytes, device);
@@ -352,18 +362,7 @@ py::tuple expert_dispatch_quant(const Tensor &x, const Tensor &rows, int scale_f
   if (h % 128 != 0) value("H must be a multiple of 128");
   require_rows(n, h);
   const c10::DeviceGuard guard(device);
-  Tensor y, s;
-  // A decode step's call is bound by the host, and a second allocation shows in it (us a
-  // call, ue8m0, 18 and 19 tokens' 8 choices of 7168, either side of the bound: 3.8 and
-  // 4.2).  Larger outputs have their own, so that one can be freed without the other.
-  if (n * h <= 1 << 20) {
-    const Tensor all = empty({n * h + n * (h / 128) * 4}, at::kByte, device);
-    y = piece(all, 0, {n, h}, at::kFloat8_e4m3fn);
-    s = piece(all, n * h / 4, {n, h / 128}, at::kFloat);
-  } else {
-    y = empty({n, h}, at::kFloat8_e4m3fn, device);
-    s = empty({n, h / 128}, at::kFloat, device);
-  }
+  const Tensor y = empty({n, h}, at::kFloat8_e4m3fn, device), s = beside(y, {n, h / 128}, at::kFloat);
   check_status(fp8_expert_dispatch_quant(x.data_ptr(), dtype, scale_fmt, c.rows, c.tokens, c.top_k, h,
                                          (uint8_t *)y.data_ptr(), (float *)s.data_ptr(), stream_of(device)));
   return py::make_tuple(y, s);

@@ -101,8 +101,8 @@ def expert_dispatch(x: torch.Tensor, rows: torch.Tensor) -> torch.Tensor:
 
 def expert_dispatch_quant(x: torch.Tensor, rows: torch.Tensor, scale_fmt=None):
     """``act_quant(expert_dispatch(x, rows), 128, scale_fmt)``, each token quantized
-    once: ``y`` (float8_e4m3fn [n, H]) and ``s`` (float32 [n, H / 128]), up to 2^20 codes
-    in one allocation.  Autograd does not see this call, nor the products'."""
+    once: ``y`` (float8_e4m3fn [n, H]) and ``s`` (float32 [n, H / 128]).  Autograd does
+    not see this call, nor the products'."""
     return _ffn_lib.ext().expert_dispatch_quant(x, rows, _format(scale_fmt))
 
 
