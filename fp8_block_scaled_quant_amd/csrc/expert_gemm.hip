@@ -697,7 +697,8 @@ __global__ __launch_bounds__(kLongThreads) void product_long_kernel(const Produc
 // (4 x 8 MFMA tiles, two waves per SIMD); gated, in each half 64 gate rows and the
 // 64 up rows of the same features.  A two-stage LDS ring by direct global->LDS
 // transfers, block kb + 1 loaded while kb is computed, over the ends of tiles.
-// The rescale of an MFMA's partial runs three MFMAs behind it.  Waves whose rows an
+// The rescale of an MFMA's partial runs three MFMAs behind it.  The loop over K is that
+// of big_tiles (e4m3_tiles.h), and a fix to one belongs in both.  Waves whose rows an
 // expert does not have skip their MFMAs: a tile of up to 128 rows keeps one wave a
 // SIMD.
 //
